@@ -268,6 +268,91 @@ smgemm_status quantize_fp8_blockwise(const float* X, int64_t rows, int64_t cols,
                                      smgemm_layout layout_x, int64_t ldx, int group_rows,
                                      uint8_t* Q, float* scales, smgemm_stream_t stream);
 
+/*
+ * quantize_int8_rowwise: 16- or 32-bit float -> int8 codes + one FP32 scale per row
+ * (per-token activation scales; for a weight stored [N][K], per-output-channel scales).
+ * For each row: amax = max|x|, s = amax/127 (IEEE FP32 division; s = 1 for an all-zero
+ * row, at least 2^-126), q = x/s (correctly rounded) rounded to the nearest integer, ties
+ * to even: |q| <= 127. Bit-exact and deterministic.
+ *   X      device, x_dtype SMGEMM_F32 / SMGEMM_BF16 / SMGEMM_F16, [rows][cols] row-major,
+ *          ldx >= cols.
+ *   Q      device int8 [rows][cols], ldq >= cols and a multiple of 16; bytes of a row past
+ *          cols are not written. scales: device float [rows]. cols == 0 writes scales of 1.
+ * A row that holds NaN or infinity gets that as its scale, so products with it are NaN or
+ * infinite; its codes are unspecified.
+ */
+smgemm_status quantize_int8_rowwise(const void* X, smgemm_dtype x_dtype, int64_t rows, int64_t cols, int64_t ldx,
+                                    int8_t* Q, int64_t ldq, float* scales, smgemm_stream_t stream);
+
+/*
+ * gemm_int8_scaled: C[m,n] = cast_c( act( sa[m] * sb[n] * sum_k Aq[m,k] * Bq[n,k] + bias[n] ) ).
+ *
+ * 8-bit integer product with a scale per token and per output channel; the sum is exact
+ * (int32; any codes -128..127, K <= 131071, else SMGEMM_ERR_UNSUPPORTED), then converted to
+ * FP32 (nearest), scaled, and finished as in gemm_bf16.
+ *   Aq  device int8 [M][K], K contiguous, lda >= K; Bq device int8 [N][K] (the weight
+ *       transposed), ldb >= K; both pitches multiples of 16. sa: device float [M], sb: [N].
+ *   bias/act/C/ldc as in gemm_bf16. workspace: smgemm_ragged_workspace_size(1, M, N, K, 1)
+ *       bytes, 16-byte aligned, used and shared as in gemm_bf16. Deterministic.
+ */
+smgemm_status gemm_int8_scaled(int64_t M, int64_t N, int64_t K, const int8_t* Aq, int64_t lda, const float* sa,
+                               const int8_t* Bq, int64_t ldb, const float* sb, const void* bias,
+                               smgemm_dtype bias_dtype, smgemm_act act, void* C, smgemm_dtype c_dtype, int64_t ldc,
+                               void* workspace, size_t workspace_bytes, smgemm_stream_t stream);
+
+/*
+ * gemm_bf16_ragged: for every expert e < E and row t with offsets[e] <= t < offsets[e+1]:
+ *   C[t, :] = cast_c( act( A[t, :] * B_e + bias[e, :] ) ),
+ * the products of a mixture-of-experts layer on rows sorted by expert, in one launch. Unlike
+ * gemm_bf16_grouped the group sizes are DEVICE data (a router's output): the host neither
+ * waits for them nor changes its arguments with them, so the call can be captured in a
+ * CUDA graph and replayed with other offsets.
+ *   offsets  device int32 [E+1], non-decreasing, within 0..T. Rows before offsets[0] and
+ *            from offsets[E] on are not written. (Offsets outside that are clamped to
+ *            [0, T] and to their running maximum: no access leaves A or C.) E <= 1024, else
+ *            SMGEMM_ERR_UNSUPPORTED.
+ *   A        device, SMGEMM_BF16 or SMGEMM_F16, [T][K] row-major, lda >= K.
+ *   B        device, same type: E matrices [K,N] in layout_b with leading dimension ldb, stride_b
+ *            elements apart (stride_b*2 a multiple of 16; the matrices must not overlap).
+ *            Row-major for a forward product; the same weights as column-major [N,K]^T give
+ *            the input gradient dX = dY * B_e^T.
+ *   bias     device, nullable, [E][N]; act, C, ldc as in gemm_bf16. K == 0 writes act(bias).
+ *   workspace  smgemm_ragged_workspace_size(E, T, N, K, 0) bytes, 16-byte aligned, used and
+ *            shared as in gemm_bf16.
+ * Deterministic; a row's result depends on its expert's rows and on the tiles of the whole
+ * call only in the order of its FP32 sums.
+ *
+ * gemm_int8_ragged: the same with int8 codes and scales as in gemm_int8_scaled:
+ *   C[t, n] = cast_c( act( sa[t] * sb[e, n] * sum_k Aq[t, k] * Bq_e[n, k] + bias[e, n] ) ),
+ *   Aq [T][K], sa [T], Bq E matrices [N][K] (ldb, stride_b), sb [E][N]; workspace kind 1.
+ *
+ * gemm_bf16_ragged_wgrad: the weight gradients, for every expert e < E:
+ *   dB_e[k, n] = cast_c( sum over its rows t of A[t, k] * D[t, n] ), zeros for no rows;
+ *   dbias[e, n] = sum over its rows t of D[t, n]  (nullable: not computed).
+ *   A [T][K], D [T][N] row-major 16-bit; dB: E row-major matrices [K][N], ldc, stride_c
+ *   elements apart (not overlapping); dbias: device float [E][N]. workspace kind 2.
+ *   Rows of no expert (padding) do not contribute, whatever they hold.
+ */
+smgemm_status gemm_bf16_ragged(int E, int64_t T, int64_t N, int64_t K, const int32_t* offsets, const void* A,
+                               smgemm_dtype ab_dtype, int64_t lda, const void* B, smgemm_layout layout_b, int64_t ldb,
+                               int64_t stride_b, const void* bias, smgemm_dtype bias_dtype, smgemm_act act, void* C,
+                               smgemm_dtype c_dtype, int64_t ldc, void* workspace, size_t workspace_bytes,
+                               smgemm_stream_t stream);
+smgemm_status gemm_int8_ragged(int E, int64_t T, int64_t N, int64_t K, const int32_t* offsets, const int8_t* Aq,
+                               int64_t lda, const float* sa, const int8_t* Bq, int64_t ldb, int64_t stride_b,
+                               const float* sb, const void* bias, smgemm_dtype bias_dtype, smgemm_act act, void* C,
+                               smgemm_dtype c_dtype, int64_t ldc, void* workspace, size_t workspace_bytes,
+                               smgemm_stream_t stream);
+smgemm_status gemm_bf16_ragged_wgrad(int E, int64_t T, int64_t N, int64_t K, const int32_t* offsets, const void* A,
+                                     smgemm_dtype ab_dtype, int64_t lda, const void* D, int64_t ldd, void* dB,
+                                     smgemm_dtype c_dtype, int64_t ldc, int64_t stride_c, float* dbias,
+                                     void* workspace, size_t workspace_bytes, smgemm_stream_t stream);
+
+/* Bytes of workspace of the ragged and int8 products. kind: 0 = gemm_bf16_ragged, 1 =
+ * gemm_int8_ragged and (with E = 1, T = M) gemm_int8_scaled, 2 = gemm_bf16_ragged_wgrad.
+ * Depends only on the arguments and the current device, not on the offsets. */
+size_t smgemm_ragged_workspace_size(int E, int64_t T, int64_t N, int64_t K, int kind);
+
 /* Bytes of workspace a call with these sizes needs (0 when none). kind: 0 = gemm_bf16,
  * 1 = gemm_fp8_blockscaled. Depends only on the arguments and the current device. */
 size_t smgemm_workspace_size(int64_t M, int64_t N, int64_t K, int kind);

@@ -12,6 +12,10 @@ is raised.
     Q, S = sg.quantize_fp8_blockwise(X, group_rows=1)
     C = sg.gemm_fp8_blockscaled(Aq, sa, Bq, sb, out_dtype=torch.bfloat16)
     Cs = sg.gemm_bf16_grouped([A0, A1], [B0, B1])
+    Xq, sx = sg.quantize_int8_rowwise(X)                       # int8 codes, a scale per row
+    C = sg.gemm_int8_scaled(Xq, sx, Wq, sw)                    # Wq[N, K], sw[N]
+    H = sg.gemm_bf16_ragged(X, W, offsets)                     # rows sorted by expert, W[E, K, N]
+    dW = sg.gemm_bf16_ragged_wgrad(X, dH, offsets)             # dX: gemm_bf16_ragged(dH, W.mT, offsets)
 """
 from __future__ import annotations
 
@@ -84,6 +88,18 @@ def lib():
             L.gemm_bf16_lse_partials.restype = I
             L.logsoftmax_apply_partials.argtypes = [P, I64, I64, I64, P, I64, P, P]
             L.logsoftmax_apply_partials.restype = I
+            L.quantize_int8_rowwise.argtypes = [P, I, I64, I64, I64, P, I64, P, P]
+            L.quantize_int8_rowwise.restype = I
+            L.gemm_int8_scaled.argtypes = [I64, I64, I64, P, I64, P, P, I64, P, P, I, I, P, I, I64, P, SZ, P]
+            L.gemm_int8_scaled.restype = I
+            L.gemm_bf16_ragged.argtypes = [I, I64, I64, I64, P, P, I, I64, P, I, I64, I64, P, I, I, P, I, I64, P, SZ, P]
+            L.gemm_bf16_ragged.restype = I
+            L.gemm_int8_ragged.argtypes = [I, I64, I64, I64, P, P, I64, P, P, I64, I64, P, P, I, I, P, I, I64, P, SZ, P]
+            L.gemm_int8_ragged.restype = I
+            L.gemm_bf16_ragged_wgrad.argtypes = [I, I64, I64, I64, P, P, I, I64, P, I64, P, I, I64, I64, P, P, SZ, P]
+            L.gemm_bf16_ragged_wgrad.restype = I
+            L.smgemm_ragged_workspace_size.argtypes = [I, I64, I64, I64, I]
+            L.smgemm_ragged_workspace_size.restype = SZ
             _lib = L
     return _lib
 
@@ -623,6 +639,267 @@ def quantize_fp8_blockwise(X, group_rows: int = 1, *, Q=None, scales=None, strea
                                       scales.data_ptr(), _stream(stream))
     _check(st, "quantize_fp8_blockwise")
     return Q, scales
+
+
+# The int8 and ragged products. Outputs and workspaces that such a call allocates belong to
+# the stream it runs on, and a call captured in a CUDA graph gets a workspace of the graph's
+# own, so that two captured graphs (or a graph and eager calls) may run side by side.
+
+def _capturing() -> bool:
+    torch = _torch()
+    return torch.cuda.is_current_stream_capturing()
+
+
+def _empty_on(stream, shape, dtype, device):
+    """torch.empty, allocated for use on `stream` (None: the current one)."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        handle = int(getattr(stream, "value", stream) or 0)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _pitched_on(stream, lead, cols, dtype, device):
+    """An uninitialised tensor [*lead, cols] whose rows start on 16-byte boundaries."""
+    unit = {_torch().float32: 4, _torch().int8: 16}.get(dtype, 8)
+    return _empty_on(stream, (*lead, -(-cols // unit) * unit), dtype, device)[..., :cols]
+
+
+def _ragged_workspace(E, T, N, K, kind, workspace, stream, sh, device):
+    if workspace is not None:
+        return workspace, _ws_bytes(workspace)
+    nbytes = int(lib().smgemm_ragged_workspace_size(E, T, N, K, kind))
+    if nbytes == 0:
+        return None, 0
+    if _capturing():
+        return _empty_on(stream, (nbytes,), _torch().uint8, device), nbytes
+    if stream is None:
+        return _workspace(nbytes, device, sh)
+    key = (device.index, int(getattr(sh, "value", sh) or 0))
+    ws = _ws_cache.get(key)
+    if ws is None or ws.numel() < nbytes:
+        if ws is not None:
+            _ws_retired.append(ws)
+        ws = _ws_cache[key] = _empty_on(stream, (max(nbytes, 0 if ws is None else 2 * ws.numel()),), _torch().uint8,
+                                        device)
+    return ws, ws.numel()
+
+
+def _rows_ld(t, name):
+    """Leading dimension of a 2-D tensor whose rows are contiguous. A single row's pitch
+    addresses nothing and is rounded up to 16 elements (whole 16-byte units)."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    rows, cols = t.shape
+    s0, s1 = t.stride()
+    if rows <= 1 or cols == 0:
+        if cols > 1 and s1 != 1:
+            raise ValueError(f"{name} must be row-major (contiguous rows)")
+        return -(-max(cols, 1) // 16) * 16
+    if (cols > 1 and s1 != 1) or s0 < cols:
+        raise ValueError(f"{name} must be row-major (contiguous rows)")
+    return s0
+
+
+def _expert_layout(t, name):
+    """(layout, leading dimension, distance between matrices) of a 3-D tensor [E, rows, cols]."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be 3-D [E, rows, cols]")
+    E, rows, cols = t.shape
+    if E == 0 or rows == 0 or cols == 0:
+        return ROW_MAJOR, -(-max(cols, 1) // 16) * 16, 0
+    s = t.stride(0)
+    if t.stride(2) == 1 and (rows <= 1 or t.stride(1) >= cols):
+        return ROW_MAJOR, (max(t.stride(1), cols) if rows > 1 else -(-cols // 16) * 16), s
+    if t.stride(1) == 1 and (cols <= 1 or t.stride(2) >= rows):
+        return COL_MAJOR, (max(t.stride(2), rows) if cols > 1 else -(-rows // 16) * 16), s
+    raise ValueError(f"{name} must have a unit stride in one of its last two dimensions")
+
+
+def _check_offsets(offsets, E):
+    torch = _torch()
+    _need(offsets.dtype == torch.int32, "offsets must be int32")
+    _need(offsets.dim() == 1 and offsets.is_contiguous(), "offsets must be a contiguous vector")
+    if offsets.shape[0] != E + 1:
+        raise ValueError(f"offsets must have E + 1 = {E + 1} elements, not {offsets.shape[0]}")
+
+
+def _scales(t, shape, name):
+    _shape(t, shape, name)
+    _dense(t, name)
+    _need(t.dtype == _torch().float32, f"{name} must be float32")
+
+
+def _expert_bias(bias, E, N):
+    if bias is None:
+        return None, 0
+    _shape(bias, (E, N), "bias")
+    _dense(bias, "bias")
+    return bias.data_ptr(), _dtype_code(bias.dtype)
+
+
+def _act_code(act):
+    if act not in ACTS:
+        raise ValueError(f"unknown activation {act!r}")
+    return ACTS[act]
+
+
+def quantize_int8_rowwise(X, *, Q=None, scales=None, stream=None):
+    """X[rows, cols] (float32, bfloat16 or float16, contiguous rows) -> (codes int8 [rows,
+    cols], scales float32 [rows]): s = amax|x| / 127 per row (1 for an all-zero row), codes
+    round-half-even(x / s). The codes' row pitch is a multiple of 16; ``Q`` and ``scales``
+    are allocated when not given."""
+    dev = _device(X, Q, scales)
+    if dev != _current_device():
+        with _torch().cuda.device(dev):
+            return quantize_int8_rowwise(X, Q=Q, scales=scales, stream=stream)
+    torch = _torch()
+    ldx = _rows_ld(X, "X")
+    rows, cols = X.shape
+    if Q is None:
+        Q = _pitched_on(stream, (rows,), cols, torch.int8, X.device)
+    if scales is None:
+        scales = _empty_on(stream, (rows,), torch.float32, X.device)
+    _shape(Q, (rows, cols), "Q")
+    _need(Q.dtype == torch.int8, "Q must be int8")
+    ldq = _rows_ld(Q, "Q")
+    _scales(scales, (rows,), "scales")
+    st = lib().quantize_int8_rowwise(X.data_ptr(), _dtype_code(X.dtype), rows, cols, ldx, Q.data_ptr(), ldq,
+                                     scales.data_ptr(), _stream(stream))
+    _check(st, "quantize_int8_rowwise")
+    return Q, scales
+
+
+def gemm_int8_scaled(Aq, sa, Bq, sb, *, bias=None, act="none", out=None, out_dtype=None, workspace=None, stream=None):
+    """C = act(sa[:, None] * sb * (Aq @ Bq^T) + bias) from int8 codes Aq[M, K], Bq[N, K] (row
+    pitches multiples of 16) and FP32 scales sa[M], sb[N]; the integer sums are exact.
+    ``out`` defaults to bfloat16."""
+    dev = _device(Aq, sa, Bq, sb, bias, out, workspace)
+    if dev != _current_device():
+        with _torch().cuda.device(dev):
+            return gemm_int8_scaled(Aq, sa, Bq, sb, bias=bias, act=act, out=out, out_dtype=out_dtype,
+                                    workspace=workspace, stream=stream)
+    torch = _torch()
+    lda, ldb = _rows_ld(Aq, "Aq"), _rows_ld(Bq, "Bq")
+    (M, K), (N, K2) = Aq.shape, Bq.shape
+    _need(K == K2, "Aq and Bq must agree in K")
+    _need(Aq.dtype == torch.int8 and Bq.dtype == torch.int8, "Aq and Bq must be int8 codes")
+    _scales(sa, (M,), "sa")
+    _scales(sb, (N,), "sb")
+    if bias is not None:
+        _vector(bias, N, "bias")
+    if out is None:
+        out = _pitched_on(stream, (M,), N, out_dtype or torch.bfloat16, Aq.device)
+    _out_matrix(out, M, N, "out")
+    sh = _stream(stream)
+    ws, wsb = _ragged_workspace(1, M, N, K, 1, workspace, stream, sh, Aq.device)
+    st = lib().gemm_int8_scaled(M, N, K, Aq.data_ptr(), lda, sa.data_ptr(), Bq.data_ptr(), ldb, sb.data_ptr(),
+                                None if bias is None else bias.data_ptr(),
+                                _dtype_code(bias.dtype) if bias is not None else 0, _act_code(act), out.data_ptr(),
+                                _dtype_code(out.dtype), _ldc(out, M, N), None if ws is None else ws.data_ptr(), wsb, sh)
+    _check(st, "gemm_int8_scaled")
+    return out
+
+
+def gemm_bf16_ragged(A, B, offsets, *, bias=None, act="none", out=None, out_dtype=None, workspace=None, stream=None):
+    """out[t] = act(A[t] @ B[e] + bias[e]) for the rows offsets[e] <= t < offsets[e+1] of
+    every expert e: A[T, K] bf16/f16 (contiguous rows, sorted by expert), B[E, K, N] in any
+    unit-stride layout (``B.mT`` of the forward's weights gives the input gradient), offsets
+    int32 [E + 1] on the device (never read by the host), bias [E, N]. Rows of no expert
+    keep what ``out`` held; a newly allocated ``out`` (A's dtype unless ``out_dtype``) is
+    uninitialised there."""
+    dev = _device(A, B, offsets, bias, out, workspace)
+    if dev != _current_device():
+        with _torch().cuda.device(dev):
+            return gemm_bf16_ragged(A, B, offsets, bias=bias, act=act, out=out, out_dtype=out_dtype,
+                                    workspace=workspace, stream=stream)
+    lda = _rows_ld(A, "A")
+    layout, ldb, stride_b = _expert_layout(B, "B")
+    (T, K), (E, K2, N) = A.shape, B.shape
+    if K != K2 or A.dtype != B.dtype:
+        raise ValueError("A and B must agree in K and dtype")
+    _check_offsets(offsets, E)
+    pbias, bias_dt = _expert_bias(bias, E, N)
+    if out is None:
+        out = _pitched_on(stream, (T,), N, out_dtype or A.dtype, A.device)
+    _out_matrix(out, T, N, "out")
+    sh = _stream(stream)
+    ws, wsb = _ragged_workspace(E, T, N, K, 0, workspace, stream, sh, A.device)
+    st = lib().gemm_bf16_ragged(E, T, N, K, offsets.data_ptr(), A.data_ptr(), _dtype_code(A.dtype), lda, B.data_ptr(),
+                                layout, ldb, stride_b, pbias, bias_dt, _act_code(act), out.data_ptr(),
+                                _dtype_code(out.dtype), _ldc(out, T, N), None if ws is None else ws.data_ptr(), wsb, sh)
+    _check(st, "gemm_bf16_ragged")
+    return out
+
+
+def gemm_int8_ragged(Aq, sa, Bq, sb, offsets, *, bias=None, act="none", out=None, out_dtype=None, workspace=None,
+                     stream=None):
+    """gemm_bf16_ragged from int8 codes: out[t] = act(sa[t] * sb[e] * (Aq[t] @ Bq[e]^T) +
+    bias[e]), Aq[T, K], sa[T], Bq[E, N, K] (K contiguous), sb[E, N]. ``out`` defaults to
+    bfloat16."""
+    dev = _device(Aq, sa, Bq, sb, offsets, bias, out, workspace)
+    if dev != _current_device():
+        with _torch().cuda.device(dev):
+            return gemm_int8_ragged(Aq, sa, Bq, sb, offsets, bias=bias, act=act, out=out, out_dtype=out_dtype,
+                                    workspace=workspace, stream=stream)
+    torch = _torch()
+    lda = _rows_ld(Aq, "Aq")
+    layout, ldb, stride_b = _expert_layout(Bq, "Bq")
+    _need(layout == ROW_MAJOR or Bq.numel() == 0, "Bq must be [E, N, K] with contiguous K")
+    (T, K), (E, N, K2) = Aq.shape, Bq.shape
+    _need(K == K2, "Aq and Bq must agree in K")
+    _need(Aq.dtype == torch.int8 and Bq.dtype == torch.int8, "Aq and Bq must be int8 codes")
+    _scales(sa, (T,), "sa")
+    _scales(sb, (E, N), "sb")
+    _check_offsets(offsets, E)
+    pbias, bias_dt = _expert_bias(bias, E, N)
+    if out is None:
+        out = _pitched_on(stream, (T,), N, out_dtype or torch.bfloat16, Aq.device)
+    _out_matrix(out, T, N, "out")
+    sh = _stream(stream)
+    ws, wsb = _ragged_workspace(E, T, N, K, 1, workspace, stream, sh, Aq.device)
+    st = lib().gemm_int8_ragged(E, T, N, K, offsets.data_ptr(), Aq.data_ptr(), lda, sa.data_ptr(), Bq.data_ptr(), ldb,
+                                stride_b, sb.data_ptr(), pbias, bias_dt, _act_code(act), out.data_ptr(),
+                                _dtype_code(out.dtype), _ldc(out, T, N), None if ws is None else ws.data_ptr(), wsb, sh)
+    _check(st, "gemm_int8_ragged")
+    return out
+
+
+def gemm_bf16_ragged_wgrad(A, D, offsets, *, out=None, out_dtype=None, dbias=None, workspace=None, stream=None):
+    """Weight gradients of gemm_bf16_ragged: out[e] = A[rows of e]^T @ D[rows of e] for A[T, K],
+    D[T, N] (bf16/f16, contiguous rows), [E, K, N] (A's dtype unless ``out`` or
+    ``out_dtype`` says otherwise), zeros for an expert without rows. ``dbias`` (float32
+    [E, N], optional) receives the sums of D's rows. Returns ``out``."""
+    dev = _device(A, D, offsets, out, dbias, workspace)
+    if dev != _current_device():
+        with _torch().cuda.device(dev):
+            return gemm_bf16_ragged_wgrad(A, D, offsets, out=out, out_dtype=out_dtype, dbias=dbias,
+                                          workspace=workspace, stream=stream)
+    lda, ldd = _rows_ld(A, "A"), _rows_ld(D, "D")
+    (T, K), (T2, N) = A.shape, D.shape
+    if T != T2 or A.dtype != D.dtype:
+        raise ValueError("A and D must agree in rows and dtype")
+    _need(offsets.dim() == 1 and offsets.shape[0] >= 1, "offsets must be a vector of E + 1 elements")
+    E = offsets.shape[0] - 1
+    _check_offsets(offsets, E)
+    if out is None:
+        out = _pitched_on(stream, (E, K), N, out_dtype or A.dtype, A.device)
+    _shape(out, (E, K, N), "out")
+    layout, ldc, stride_c = _expert_layout(out, "out")
+    _need(layout == ROW_MAJOR, "out must be row-major matrices")
+    if dbias is not None:
+        _scales(dbias, (E, N), "dbias")
+    sh = _stream(stream)
+    ws, wsb = _ragged_workspace(E, T, N, K, 2, workspace, stream, sh, A.device)
+    st = lib().gemm_bf16_ragged_wgrad(E, T, N, K, offsets.data_ptr(), A.data_ptr(), _dtype_code(A.dtype), lda,
+                                      D.data_ptr(), ldd, out.data_ptr(), _dtype_code(out.dtype), ldc, stride_c,
+                                      None if dbias is None else dbias.data_ptr(),
+                                      None if ws is None else ws.data_ptr(), wsb, sh)
+    _check(st, "gemm_bf16_ragged_wgrad")
+    return out
 
 
 def check(stream=None) -> int:

@@ -25,6 +25,8 @@
 #include "../../include/smgemm.h"
 #include "grouped.h"
 #include "kernels.h"
+#include "ragged.h"
+#include "ragged.cuh"
 
 using namespace smg;
 
@@ -345,6 +347,46 @@ bool encode_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint6
   cache.key[slot] = k;
   cache.map[slot] = *map;
   cache.used[slot] = true;
+  return true;
+}
+
+// The same for a 3-D tensor (per-expert matrices): dims and strides innermost first, one
+// matrix per box.
+struct MapKey3 {
+  MapKey k;
+  uint64_t depth, depth_stride;
+};
+
+bool encode_3d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
+               uint64_t depth, uint64_t row_stride_bytes, uint64_t depth_stride_bytes, uint32_t box_inner,
+               uint32_t box_outer) {
+  constexpr int kEntries = 16;
+  thread_local MapKey3 keys[kEntries];
+  thread_local CUtensorMap maps[kEntries];
+  thread_local bool used[kEntries] = {};
+  thread_local int next = 0;
+  const MapKey3 k{{base, inner, outer, row_stride_bytes, box_inner, box_outer, static_cast<int>(dt), 0}, depth,
+                  depth_stride_bytes};
+  for (int i = 0; i < kEntries; ++i) {
+    if (used[i] && keys[i].k == k.k && keys[i].depth == depth && keys[i].depth_stride == depth_stride_bytes) {
+      *map = maps[i];
+      return true;
+    }
+  }
+  PFN_encodeTiled fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {inner, outer, depth};
+  const cuuint64_t strides[2] = {row_stride_bytes, depth_stride_bytes};
+  const cuuint32_t box[3] = {box_inner, box_outer, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  if (fn(map, dt, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return false;
+  keys[next] = k;
+  maps[next] = *map;
+  used[next] = true;
+  next = (next + 1) % kEntries;
   return true;
 }
 
@@ -1008,6 +1050,277 @@ smgemm_status quantize_fp8_blockwise(const float* X, int64_t rows, int64_t cols,
   return launch_status(e);
 }
 
+// ------------------------------------------------------------------ ragged products
+
+namespace {
+constexpr int64_t kInt8MaxK = 131071;  // 128 * 128 * K stays below 2^31
+
+// Token tiles of at most 64 rows when groups average at most 32 rows: the call then streams
+// the weights (memory bound), and the smaller row tiles leave shared memory for more stages
+// of weight loads in flight; above, 256 rows reuse each weight tile four times as often.
+bool ragged_narrow(int E, int64_t T) { return T <= 64 || T <= 32 * static_cast<int64_t>(E); }
+
+size_t ragged_counter_bytes(int clusters) {
+  return (static_cast<size_t>(clusters) * 2 * sizeof(unsigned long long) + 255) / 256 * 256;
+}
+
+// Counters, then two partial tiles per cluster (a stream-K range cuts at most its first and
+// last tile) of 256 x TN; the weight gradient needs one of 256 x 256.
+size_t ragged_ws_bytes(int clusters, int tn, int slots_per_cluster) {
+  return ragged_counter_bytes(clusters) +
+         static_cast<size_t>(clusters) * slots_per_cluster * 2 * 128 * static_cast<size_t>(tn) * sizeof(float);
+}
+
+smgemm_status check_groups(int E, int64_t T, int64_t N, int64_t K, const int32_t* offsets) {
+  if (E < 0 || !fits_int(T) || !fits_int(N) || !fits_int(K)) return SMGEMM_ERR_INVALID_ARG;
+  if (E > kRaggedMaxGroups) return SMGEMM_ERR_UNSUPPORTED;
+  if (E > 0 && offsets == nullptr) return SMGEMM_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(offsets) & 3u) return SMGEMM_ERR_ALIGNMENT;
+  return SMGEMM_OK;
+}
+
+// Distance between the experts' matrices, each of `rows` rows `ld` apart: no overlap.
+bool valid_group_stride(int E, int64_t stride, int64_t rows, int64_t cols, int64_t ld) {
+  return E <= 1 || stride >= (rows - 1) * ld + cols;
+}
+
+struct RaggedArgs {
+  const char* path;
+  int E;
+  int64_t T, N, K;
+  const int32_t* offsets;
+  const void* A;
+  int ab_dtype;  // kBF16 / kF16, or -1: int8
+  int64_t lda;
+  const float* sa;
+  const void* B;
+  int layout_b;
+  int64_t ldb, stride_b;
+  const float* sb;
+  const void* bias;
+  int bias_dtype, act;
+  void* C;
+  int c_dtype;
+  int64_t ldc;
+};
+
+smgemm_status ragged_impl(const RaggedArgs& a, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  const bool i8 = a.ab_dtype < 0;
+  const int64_t esz = i8 ? 1 : 2;
+  if (!valid_layout(a.layout_b)) return SMGEMM_ERR_INVALID_ARG;
+  if (!valid_out_dtype(a.c_dtype) || !valid_act(a.act)) return SMGEMM_ERR_INVALID_ARG;
+  if (a.E == 0 || a.T == 0 || a.N == 0) return SMGEMM_OK;
+  const smgemm_status st = check_output(a.T, a.N, a.C, a.c_dtype, a.ldc, a.bias, a.bias_dtype, a.act);
+  if (st != SMGEMM_OK) return st;
+  const bool w_mn = a.layout_b == SMGEMM_ROW_MAJOR;
+  if (i8 && a.K > kInt8MaxK) return SMGEMM_ERR_UNSUPPORTED;
+  if (a.K > 0) {
+    if (a.A == nullptr || a.B == nullptr || (i8 && (a.sa == nullptr || a.sb == nullptr))) return SMGEMM_ERR_INVALID_ARG;
+    if (a.lda < a.K || a.ldb < (w_mn ? a.N : a.K)) return SMGEMM_ERR_INVALID_ARG;
+    if (!valid_group_stride(a.E, a.stride_b, w_mn ? a.K : a.N, w_mn ? a.N : a.K, a.ldb)) return SMGEMM_ERR_INVALID_ARG;
+    if (!aligned16(a.A) || !aligned16(a.B) || (a.lda * esz) % 16 != 0 || (a.ldb * esz) % 16 != 0 ||
+        (a.E > 1 && (a.stride_b * esz) % 16 != 0))
+      return SMGEMM_ERR_ALIGNMENT;
+    if (i8 && ((reinterpret_cast<uintptr_t>(a.sa) & 3u) || (reinterpret_cast<uintptr_t>(a.sb) & 3u)))
+      return SMGEMM_ERR_ALIGNMENT;
+  }
+  const bool narrow = ragged_narrow(a.E, a.T);
+  const int tn = ragged_tile_tokens(narrow);
+  const int64_t n_ft = (a.N + 255) / 256;
+  if ((std::min<int64_t>(a.E, a.T) + a.T / 32) * n_ft > 0x7FFFFFFF) return SMGEMM_ERR_INVALID_ARG;  // tile numbers are 32-bit
+  DevInfo d;
+  if (current_device(d) != SMGEMM_OK) return SMGEMM_ERR_CUDA;
+  const int P = ragged_max_clusters();
+  if (P <= 0) return SMGEMM_ERR_CUDA;
+  if (workspace == nullptr || workspace_bytes < ragged_ws_bytes(P, tn, 2)) return SMGEMM_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return SMGEMM_ERR_ALIGNMENT;
+
+  RaggedMaps m;
+  std::memset(&m, 0, sizeof(m));
+  RaggedParams p{};
+  const int bke = i8 ? 128 : 64;
+  if (a.K > 0) {
+    const CUtensorMapDataType dt = i8                      ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : a.ab_dtype == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                           : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const uint64_t depth_stride =
+        static_cast<uint64_t>(a.E > 1 ? a.stride_b : (w_mn ? a.K : a.N) * a.ldb) * static_cast<uint64_t>(esz);
+    bool ok = w_mn ? encode_3d(&m.w, dt, a.B, a.N, a.K, a.E, a.ldb * esz, depth_stride, 64, 64)
+                   : encode_3d(&m.w, dt, a.B, a.K, a.N, a.E, a.ldb * esz, depth_stride, bke, 128);
+    for (int i = 0; i < 3; ++i) ok = ok && encode_2d(&m.x[i], dt, a.A, a.K, a.T, a.lda * esz, bke, 64 >> i);
+    if (!ok) return SMGEMM_ERR_CUDA;
+  }
+  const uint32_t fmt = a.ab_dtype == kBF16 ? 1u : 0u;
+  p.offsets = a.offsets;
+  p.E = a.E;
+  p.T = static_cast<int>(a.T);
+  p.N = static_cast<int>(a.N);
+  p.kb_total = static_cast<int>((a.K + bke - 1) / bke);
+  p.n_ft = static_cast<int>(n_ft);
+  p.w_mn_major = w_mn ? 1 : 0;
+  p.idesc = i8 ? idesc_i8(256, 0) : idesc_f32acc(fmt, fmt, w_mn ? 1u : 0u, 0u, 256, 0);
+  p.bias = a.bias;
+  p.bias_dtype = a.bias_dtype;
+  p.act = a.act;
+  p.C = a.C;
+  p.c_dtype = a.c_dtype;
+  p.ldc = a.ldc;
+  p.sa = a.sa;
+  p.sb = a.sb;
+  p.counters = static_cast<unsigned long long*>(workspace);
+  p.slots = reinterpret_cast<float*>(static_cast<char*>(workspace) + ragged_counter_bytes(P));
+  p.gen = next_generation();
+  p.wait_limit_cycles = wait_limit();
+  // The tile count depends on the offsets: launch as many clusters as the most tiles and
+  // K pieces there can be.
+  const int64_t most = (std::min<int64_t>(a.E, a.T) + a.T / 32) * n_ft * std::max(1, p.kb_total / 4);
+  const int clusters = static_cast<int>(std::min<int64_t>(most, P));
+  std::snprintf(config_text(), sizeof(g_last_config), "path=%s groups=%d rows=%d kb=%d grid=%d tile=256x%d", a.path,
+                a.E, p.T, p.kb_total, clusters, tn);
+  if (env_ll(kKnobLog, 0)) std::fprintf(stderr, "[smgemm] %s\n", g_last_config);
+  return launch_status(launch_gemm_ragged(m, p, i8, narrow, clusters, stream));
+}
+}  // namespace
+
+size_t smgemm_ragged_workspace_size(int E, int64_t T, int64_t N, int64_t K, int kind) {
+  refresh_knobs();
+  if (E <= 0 || T < 0 || N <= 0 || K < 0 || (kind != 2 && T == 0)) return 0;
+  DevInfo d;
+  if (current_device(d) != SMGEMM_OK) return 0;
+  if (kind == 2) return ragged_ws_bytes(wgrad_max_clusters(), 256, 1);
+  return ragged_ws_bytes(ragged_max_clusters(), ragged_tile_tokens(ragged_narrow(E, T)), 2);
+}
+
+smgemm_status gemm_bf16_ragged(int E, int64_t T, int64_t N, int64_t K, const int32_t* offsets, const void* A,
+                               smgemm_dtype ab_dtype, int64_t lda, const void* B, smgemm_layout layout_b, int64_t ldb,
+                               int64_t stride_b, const void* bias, smgemm_dtype bias_dtype, smgemm_act act, void* C,
+                               smgemm_dtype c_dtype, int64_t ldc, void* workspace, size_t workspace_bytes,
+                               smgemm_stream_t stream) {
+  const CallScope scope("smgemm:gemm_bf16_ragged");
+  const smgemm_status st = check_groups(E, T, N, K, offsets);
+  if (st != SMGEMM_OK) return st;
+  if (ab_dtype != SMGEMM_BF16 && ab_dtype != SMGEMM_F16) return SMGEMM_ERR_UNSUPPORTED;
+  const RaggedArgs a{"ragged", E,   T,        N,       K,    offsets,    A,   ab_dtype, lda,     nullptr, B,
+                     layout_b, ldb, stride_b, nullptr, bias, bias_dtype, act, C,        c_dtype, ldc};
+  return ragged_impl(a, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+smgemm_status gemm_int8_ragged(int E, int64_t T, int64_t N, int64_t K, const int32_t* offsets, const int8_t* Aq,
+                               int64_t lda, const float* sa, const int8_t* Bq, int64_t ldb, int64_t stride_b,
+                               const float* sb, const void* bias, smgemm_dtype bias_dtype, smgemm_act act, void* C,
+                               smgemm_dtype c_dtype, int64_t ldc, void* workspace, size_t workspace_bytes,
+                               smgemm_stream_t stream) {
+  const CallScope scope("smgemm:gemm_int8_ragged");
+  const smgemm_status st = check_groups(E, T, N, K, offsets);
+  if (st != SMGEMM_OK) return st;
+  const RaggedArgs a{"int8-ragged",    E,   T,        N,  K,    offsets,    Aq,  -1, lda,     sa, Bq,
+                     SMGEMM_COL_MAJOR, ldb, stride_b, sb, bias, bias_dtype, act, C,  c_dtype, ldc};
+  return ragged_impl(a, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+smgemm_status gemm_int8_scaled(int64_t M, int64_t N, int64_t K, const int8_t* Aq, int64_t lda, const float* sa,
+                               const int8_t* Bq, int64_t ldb, const float* sb, const void* bias,
+                               smgemm_dtype bias_dtype, smgemm_act act, void* C, smgemm_dtype c_dtype, int64_t ldc,
+                               void* workspace, size_t workspace_bytes, smgemm_stream_t stream) {
+  const CallScope scope("smgemm:gemm_int8_scaled");
+  if (!fits_int(M) || !fits_int(N) || !fits_int(K)) return SMGEMM_ERR_INVALID_ARG;
+  const RaggedArgs a{"int8", 1,   M, N,  K,    nullptr,    Aq,  -1, lda,     sa, Bq, SMGEMM_COL_MAJOR,
+                     ldb,    0, sb, bias, bias_dtype, act, C,  c_dtype, ldc};
+  return ragged_impl(a, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+smgemm_status gemm_bf16_ragged_wgrad(int E, int64_t T, int64_t N, int64_t K, const int32_t* offsets, const void* A,
+                                     smgemm_dtype ab_dtype, int64_t lda, const void* D, int64_t ldd, void* dB,
+                                     smgemm_dtype c_dtype, int64_t ldc, int64_t stride_c, float* dbias,
+                                     void* workspace, size_t workspace_bytes, smgemm_stream_t stream_) {
+  const CallScope scope("smgemm:gemm_bf16_ragged_wgrad");
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  smgemm_status st = check_groups(E, T, N, K, offsets);
+  if (st != SMGEMM_OK) return st;
+  if (ab_dtype != SMGEMM_BF16 && ab_dtype != SMGEMM_F16) return SMGEMM_ERR_UNSUPPORTED;
+  if (!valid_out_dtype(c_dtype)) return SMGEMM_ERR_INVALID_ARG;
+  if (E == 0 || N == 0) return SMGEMM_OK;
+  if (T > 0) {
+    if ((K > 0 && (A == nullptr || lda < K)) || D == nullptr || ldd < N) return SMGEMM_ERR_INVALID_ARG;
+    if (!aligned16(A) || !aligned16(D) || (lda * 2) % 16 != 0 || (ldd * 2) % 16 != 0) return SMGEMM_ERR_ALIGNMENT;
+  }
+  if (reinterpret_cast<uintptr_t>(dbias) & 3u) return SMGEMM_ERR_ALIGNMENT;
+  const int64_t m_tiles = (K + 255) / 256, n_tiles = (N + 255) / 256;
+  if (K > 0) {
+    st = check_output(K, N, dB, c_dtype, ldc, nullptr, 0, 0);
+    if (st != SMGEMM_OK) return st;
+    if (!valid_group_stride(E, stride_c, K, N, ldc)) return SMGEMM_ERR_INVALID_ARG;
+    if (E > 1 && (stride_c * elem_size(c_dtype)) % 16 != 0) return SMGEMM_ERR_ALIGNMENT;
+    if (m_tiles * n_tiles > 0x7FFFFFFF / E) return SMGEMM_ERR_INVALID_ARG;  // tile numbers are 32-bit
+  }
+  DevInfo d;
+  if (current_device(d) != SMGEMM_OK) return SMGEMM_ERR_CUDA;
+  const bool bf16 = ab_dtype == SMGEMM_BF16;
+  if (K > 0) {
+    const int P = wgrad_max_clusters();
+    if (P <= 0) return SMGEMM_ERR_CUDA;
+    if (workspace == nullptr || workspace_bytes < ragged_ws_bytes(P, 256, 1)) return SMGEMM_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return SMGEMM_ERR_ALIGNMENT;
+    WgradMaps m;
+    std::memset(&m, 0, sizeof(m));
+    if (T > 0) {
+      const CUtensorMapDataType dt = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+      for (int i = 0; i < kWgradBoxes; ++i)
+        if (!encode_2d(&m.a[i], dt, A, K, T, lda * 2, 64, 64 >> i) || !encode_2d(&m.d[i], dt, D, N, T, ldd * 2, 64, 64 >> i))
+          return SMGEMM_ERR_CUDA;
+    }
+    const uint32_t fmt = bf16 ? 1u : 0u;
+    WgradParams p{};
+    p.offsets = offsets;
+    p.E = E;
+    p.T = static_cast<int>(T);
+    p.K = static_cast<int>(K);
+    p.N = static_cast<int>(N);
+    p.m_tiles = static_cast<int>(m_tiles);
+    p.n_tiles = static_cast<int>(n_tiles);
+    p.idesc = idesc_f32acc(fmt, fmt, 1u, 1u, 256, 256);
+    p.C = dB;
+    p.c_dtype = c_dtype;
+    p.ldc = ldc;
+    p.stride_c = stride_c;
+    p.counters = static_cast<unsigned long long*>(workspace);
+    p.slots = reinterpret_cast<float*>(static_cast<char*>(workspace) + ragged_counter_bytes(P));
+    p.gen = next_generation();
+    p.wait_limit_cycles = wait_limit();
+    // Up to T / 512 pieces of one tile's rows run side by side.
+    const int64_t most = E * m_tiles * n_tiles * std::max<int64_t>(1, T / 512);
+    const int clusters = static_cast<int>(std::min<int64_t>(most, P));
+    std::snprintf(config_text(), sizeof(g_last_config), "path=ragged-wgrad groups=%d rows=%d tiles=%dx%d grid=%d", E,
+                  p.T, p.m_tiles, p.n_tiles, clusters);
+    if (env_ll(kKnobLog, 0)) std::fprintf(stderr, "[smgemm] %s\n", g_last_config);
+    st = launch_status(launch_gemm_ragged_wgrad(m, p, clusters, stream));
+    if (st != SMGEMM_OK) return st;
+  }
+  if (dbias == nullptr) return SMGEMM_OK;
+  return launch_status(
+      launch_ragged_dbias(D, bf16, ldd, static_cast<int>(T), static_cast<int>(N), offsets, E, dbias, stream));
+}
+
+smgemm_status quantize_int8_rowwise(const void* X, smgemm_dtype x_dtype, int64_t rows, int64_t cols, int64_t ldx,
+                                    int8_t* Q, int64_t ldq, float* scales, smgemm_stream_t stream) {
+  const CallScope scope("smgemm:quantize_int8_rowwise");
+  if (!fits_int(rows) || !fits_int(cols)) return SMGEMM_ERR_INVALID_ARG;
+  if (!valid_out_dtype(x_dtype)) return SMGEMM_ERR_UNSUPPORTED;
+  if (rows == 0) return SMGEMM_OK;
+  if (scales == nullptr) return SMGEMM_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(scales) & 3u) return SMGEMM_ERR_ALIGNMENT;
+  if (cols > 0) {  // rows without elements only get their scale, 1
+    if (X == nullptr || Q == nullptr || ldx < cols || ldq < cols) return SMGEMM_ERR_INVALID_ARG;
+    if (!aligned16(X) || !aligned16(Q) || (ldx * elem_size(x_dtype)) % 16 != 0 || ldq % 16 != 0)
+      return SMGEMM_ERR_ALIGNMENT;
+  }
+  DevInfo d;
+  if (current_device(d) != SMGEMM_OK) return SMGEMM_ERR_CUDA;
+  return launch_status(launch_quant_int8(X, x_dtype, ldx * elem_size(x_dtype), static_cast<int>(rows),
+                                         static_cast<int>(cols), Q, ldq, scales,
+                                         reinterpret_cast<cudaStream_t>(stream)));
+}
+
 smgemm_status smgemm_check(smgemm_stream_t stream_) {
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   if (cudaStreamSynchronize(stream) != cudaSuccess) {
@@ -1015,7 +1328,8 @@ smgemm_status smgemm_check(smgemm_stream_t stream_) {
     return SMGEMM_ERR_CUDA;
   }
   const unsigned e = take_error_word_tc16() | take_error_word_fp8() | take_error_word_misc() | take_error_word_pair() |
-                     take_error_word_fp8_pair() | take_error_word_grouped();
+                     take_error_word_fp8_pair() | take_error_word_grouped() | take_error_word_ragged() |
+                     take_error_word_wgrad();
   return (e & kErrTimeout) ? SMGEMM_ERR_TIMEOUT : SMGEMM_OK;
 }
 

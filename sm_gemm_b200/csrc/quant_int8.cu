@@ -1,0 +1,221 @@
+// Row quantiser to int8: s = amax|x| / 127 over a row (IEEE FP32 division; 1 for an all-zero
+// row, never below 2^-126), q = round-half-even(x / s), the quotient correctly rounded in
+// FP32. The codes and scales are the operands of the int8 products (a token of activations
+// or, for a weight stored [N][K], an output channel per row).
+//
+// Memory bound: M K elements are read once and M K codes written, so a row stays in
+// registers between its maximum and its codes (16-byte loads, kept packed). Rows of up to
+// 128 vectors take one warp, with no barrier; longer ones one CTA, sized so that a thread
+// keeps at most 8 vectors; rows longer than 4096 vectors are read a second time (from L2).
+//
+// The maximum is taken on the bit patterns of |x|, whose order is that of the values with
+// NaN above infinity: a row that holds either gets the scale NaN or infinity, so every
+// product with it is NaN or infinite instead of silently finite (its codes are unspecified).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "fp8_codec.cuh"
+#include "kernels.h"
+#include "ragged.h"
+#include "sm100.cuh"
+
+namespace smg {
+
+namespace {
+// Rounds to the nearest integer, ties to even: in [2^23, 2^24) FP32 spacing is 1, and the
+// low byte of the sum is the integer's two's complement.
+constexpr float kRoundMagic = 12582912.0f;  // 1.5 * 2^23
+
+template <int DT>
+struct Vec {  // 16 bytes of one row
+  static constexpr int kElems = DT == kF32 ? 4 : 8;
+  uint32_t w[4];
+
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (DT == kF32) return __uint_as_float(w[i]);
+    else if constexpr (DT == kBF16) return __uint_as_float((i & 1) ? (w[i >> 1] & 0xffff0000u) : (w[i >> 1] << 16));
+    else return __half2float(__ushort_as_half(static_cast<unsigned short>(w[i >> 1] >> (16 * (i & 1)))));
+  }
+  // Largest |x| as an FP32 bit pattern.
+  __device__ __forceinline__ uint32_t amax_bits() const {
+    if constexpr (DT == kF32) {
+      const uint32_t a = max(w[0] & 0x7fffffffu, w[1] & 0x7fffffffu), b = max(w[2] & 0x7fffffffu, w[3] & 0x7fffffffu);
+      return max(a, b);
+    } else {
+      const uint32_t a = __vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu);
+      const uint32_t b = __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu);
+      const uint32_t c = __vmaxu2(a, b);
+      const uint32_t h = max(c & 0xffffu, c >> 16);
+      if constexpr (DT == kBF16) return h << 16;
+      else return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(h)))) & 0x7fffffffu;
+    }
+  }
+};
+
+template <int DT>
+__device__ __forceinline__ Vec<DT> load_vec(const void* row, int v, int K) {
+  constexpr int E = Vec<DT>::kElems;
+  Vec<DT> x;
+  if ((v + 1) * E <= K) {
+    const uint4 t = __ldg(static_cast<const uint4*>(row) + v);
+    x.w[0] = t.x; x.w[1] = t.y; x.w[2] = t.z; x.w[3] = t.w;
+  } else {  // the row's last, partial vector (or nothing): nothing past K is read
+    x.w[0] = x.w[1] = x.w[2] = x.w[3] = 0u;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int k = v * E + i;
+      if (k < K) {
+        if constexpr (DT == kF32) x.w[i] = static_cast<const uint32_t*>(row)[k];
+        else x.w[i >> 1] |= static_cast<uint32_t>(static_cast<const uint16_t*>(row)[k]) << (16 * (i & 1));
+      }
+    }
+  }
+  return x;
+}
+
+__device__ __forceinline__ uint32_t pack_low_bytes(float a, float b, float c, float d) {
+  const uint32_t lo = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0040);
+  const uint32_t hi = __byte_perm(__float_as_uint(c), __float_as_uint(d), 0x0040);
+  return __byte_perm(lo, hi, 0x5410);
+}
+
+template <int DT>
+__device__ __forceinline__ void encode_vec(const Vec<DT>& x, bool fast, const MarksteinDiv& md, int v, int K,
+                                           int8_t* q) {
+  constexpr int E = Vec<DT>::kElems;
+  uint32_t w[E / 4];
+#pragma unroll
+  for (int h = 0; h < E / 4; ++h) {
+    float y[4];
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      float2 d = make_float2(x.at(4 * h + i), x.at(4 * h + i + 1));
+      d = fast ? md.div2(d) : make_float2(__fdiv_rn(d.x, md.s), __fdiv_rn(d.y, md.s));
+      d = __fadd2_rn(d, make_float2(kRoundMagic, kRoundMagic));
+      y[i] = d.x;
+      y[i + 1] = d.y;
+    }
+    w[h] = pack_low_bytes(y[0], y[1], y[2], y[3]);
+  }
+  if ((v + 1) * E <= K) {
+    if constexpr (E == 8) *reinterpret_cast<uint2*>(q + v * E) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(q + v * E) = w[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if (v * E + i < K) q[v * E + i] = static_cast<int8_t>(w[i >> 2] >> (8 * (i & 3)));
+  }
+}
+
+__device__ __forceinline__ float int8_scale(uint32_t amax_bits) {
+  if (amax_bits == 0u) return 1.0f;
+  const float s = __fdiv_rn(__uint_as_float(amax_bits), 127.0f);
+  return s < 1.17549435e-38f ? 1.17549435e-38f : s;  // 2^-126; NaN stays NaN
+}
+
+// One warp per row, NV vectors per lane.
+template <int DT, int NV>
+__global__ void __launch_bounds__(128) quant_int8_warp_kernel(const void* __restrict__ X, long long ld_bytes, int M, int K,
+                                                              int8_t* __restrict__ Q, long long ldq,
+                                                              float* __restrict__ S) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= M) return;
+  const char* x = static_cast<const char*>(X) + row * ld_bytes;
+  Vec<DT> v[NV];
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) v[i] = load_vec<DT>(x, i * 32 + lane, K);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) top = max(top, v[i].amax_bits());
+  top = __reduce_max_sync(0xffffffffu, top);
+  const float s = int8_scale(top);
+  if (lane == 0) S[row] = s;
+  const bool fast = markstein_ok(s);
+  const MarksteinDiv md = markstein_div(s);
+  int8_t* q = Q + row * ldq;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) encode_vec<DT>(v[i], fast, md, i * 32 + lane, K, q);
+}
+
+// One CTA per row; NV vectors per thread in registers, or (NV = 0) the row read twice.
+template <int DT, int NV>
+__global__ void __launch_bounds__(512) quant_int8_cta_kernel(const void* __restrict__ X, long long ld_bytes, int K,
+                                                             int8_t* __restrict__ Q, long long ldq,
+                                                             float* __restrict__ S) {
+  __shared__ uint32_t tops[16];
+  pdl_launch_dependents();
+  pdl_wait();
+  const long long row = blockIdx.x;
+  const char* x = static_cast<const char*>(X) + row * ld_bytes;
+  const int nthr = blockDim.x, nvec = (K + Vec<DT>::kElems - 1) / Vec<DT>::kElems;
+  uint32_t top = 0;
+  Vec<DT> v[NV > 0 ? NV : 1];
+  if constexpr (NV > 0) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = load_vec<DT>(x, i * nthr + threadIdx.x, K);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) top = max(top, v[i].amax_bits());
+  } else {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < nvec; i += nthr) top = max(top, load_vec<DT>(x, i, K).amax_bits());
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
+  __syncthreads();
+  const int nwarp = nthr >> 5;
+  top = (threadIdx.x & 31) < nwarp ? tops[threadIdx.x & 31] : 0u;
+  top = __reduce_max_sync(0xffffffffu, top);
+  const float s = int8_scale(top);
+  if (threadIdx.x == 0) S[row] = s;
+  const bool fast = markstein_ok(s);
+  const MarksteinDiv md = markstein_div(s);
+  int8_t* q = Q + row * ldq;
+  if constexpr (NV > 0) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) encode_vec<DT>(v[i], fast, md, i * nthr + threadIdx.x, K, q);
+  } else {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < nvec; i += nthr) encode_vec<DT>(load_vec<DT>(x, i, K), fast, md, i, K, q);
+  }
+}
+
+template <int DT>
+cudaError_t launch_of(const void* X, long long ld_bytes, int M, int K, int8_t* Q, long long ldq, float* S,
+                      cudaStream_t stream) {
+  const int nvec = (K + Vec<DT>::kElems - 1) / Vec<DT>::kElems;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  add_pdl_attr(cfg, attr);
+  if (nvec <= 128) {
+    cfg.gridDim = dim3((M + 3) / 4, 1, 1);
+    cfg.blockDim = dim3(128, 1, 1);
+    if (nvec <= 32) return cudaLaunchKernelEx(&cfg, quant_int8_warp_kernel<DT, 1>, X, ld_bytes, M, K, Q, ldq, S);
+    return cudaLaunchKernelEx(&cfg, quant_int8_warp_kernel<DT, 4>, X, ld_bytes, M, K, Q, ldq, S);
+  }
+  cfg.gridDim = dim3(M, 1, 1);
+  const int nv = nvec <= 2048 ? 4 : 8;
+  int threads = ((nvec + nv - 1) / nv + 31) / 32 * 32;
+  threads = threads > 512 ? 512 : threads;
+  cfg.blockDim = dim3(threads, 1, 1);
+  if (nvec <= 2048) return cudaLaunchKernelEx(&cfg, quant_int8_cta_kernel<DT, 4>, X, ld_bytes, K, Q, ldq, S);
+  if (nvec <= 4096) return cudaLaunchKernelEx(&cfg, quant_int8_cta_kernel<DT, 8>, X, ld_bytes, K, Q, ldq, S);
+  return cudaLaunchKernelEx(&cfg, quant_int8_cta_kernel<DT, 0>, X, ld_bytes, K, Q, ldq, S);
+}
+}  // namespace
+
+cudaError_t launch_quant_int8(const void* X, int dtype, long long ld_bytes, int M, int K, int8_t* Q, long long ldq,
+                              float* S, cudaStream_t stream) {
+  cudaError_t e;
+  if (dtype == kF32) e = launch_of<kF32>(X, ld_bytes, M, K, Q, ldq, S, stream);
+  else if (dtype == kBF16) e = launch_of<kBF16>(X, ld_bytes, M, K, Q, ldq, S, stream);
+  else e = launch_of<kF16>(X, ld_bytes, M, K, Q, ldq, S, stream);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+}  // namespace smg

@@ -1,0 +1,76 @@
+// Products whose rows belong to experts (gemm_ragged.cu): interface between the C-ABI
+// layer and the kernels.
+#pragma once
+
+#include "kernels.h"
+
+namespace smg {
+
+constexpr int kRaggedMaxGroups = 1024;  // the group table sits in shared memory
+
+// Tensor maps of one call. w: the weights as a 3-D tensor (box 64 N x 64 K elements of one
+// expert when N is contiguous, else 128 bytes of K x 128 N). x[i]: the activation rows,
+// boxes of 128 bytes of K x (64 >> i) rows.
+struct RaggedMaps {
+  CUtensorMap w;
+  CUtensorMap x[3];
+};
+
+struct RaggedParams {
+  const int* offsets;       // device, E + 1 row offsets; nullptr: one group of rows [0, T)
+  int E, T, N;
+  int kb_total, n_ft;       // K blocks of 128 bytes; 256-feature tiles per expert
+  int w_mn_major;
+  uint32_t idesc;           // without its N field
+  const void* bias;         // nullable, [E][N]
+  int bias_dtype, act;
+  void* C;
+  int c_dtype;
+  long long ldc;
+  const float* sa;          // int8: [T] row scales
+  const float* sb;          // int8: [E][N] column scales
+  float* slots;             // partial tiles: [clusters][2][2 ranks][TN][128] 32-bit words
+  unsigned long long* counters;  // [clusters][2] arrival counters of split tiles
+  unsigned long long gen;
+  unsigned long long wait_limit_cycles;
+};
+
+// narrow: token tiles of at most 64 rows (else 256).
+cudaError_t launch_gemm_ragged(const RaggedMaps& m, const RaggedParams& p, bool i8, bool narrow, int clusters,
+                               cudaStream_t stream);
+int ragged_max_clusters();
+inline int ragged_tile_tokens(bool narrow) { return narrow ? 64 : 256; }
+unsigned take_error_word_ragged();
+
+// Weight gradients (gemm_ragged_wgrad.cu). Boxes of 64 columns x (64 >> i) rows of A and D.
+constexpr int kWgradBoxes = 7;
+struct WgradMaps {
+  CUtensorMap a[kWgradBoxes];
+  CUtensorMap d[kWgradBoxes];
+};
+
+struct WgradParams {
+  const int* offsets;       // device, E + 1 row offsets
+  int E, T, K, N;           // dB[e] is K x N
+  int m_tiles, n_tiles;     // 256 x 256 tiles of one dB[e]
+  uint32_t idesc;
+  void* C;
+  int c_dtype;
+  long long ldc, stride_c;  // elements between rows / experts of dB
+  float* slots;             // split tiles: [clusters][2 ranks][128][256] partials
+  unsigned long long* counters;  // [clusters][2]
+  unsigned long long gen;
+  unsigned long long wait_limit_cycles;
+};
+
+cudaError_t launch_gemm_ragged_wgrad(const WgradMaps& m, const WgradParams& p, int clusters, cudaStream_t stream);
+int wgrad_max_clusters();
+cudaError_t launch_ragged_dbias(const void* D, bool bf16, long long ldd, int T, int N, const int* offsets, int E,
+                                float* db, cudaStream_t stream);
+unsigned take_error_word_wgrad();
+
+// Row quantiser (quant_int8.cu): X [M][K] of dtype, rows ld_bytes apart (16-byte aligned).
+cudaError_t launch_quant_int8(const void* X, int dtype, long long ld_bytes, int M, int K, int8_t* Q, long long ldq,
+                              float* S, cudaStream_t stream);
+
+}  // namespace smg

@@ -1,0 +1,260 @@
+"""Row quantiser to int8 and the int8 products (gemm_int8_scaled, gemm_int8_ragged): codes
+bit for bit, exact integer sums, every size where a tile, a warp or a vector ends, against
+plain arithmetic in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+import sm_gemm_b200 as sg
+from _ragged import U32, act64, check_as, codes, normal, offsets_of, pitched
+
+pytestmark = pytest.mark.gpu
+
+BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+def _quant(X):
+    """The definition, with IEEE FP32 divisions (numpy)."""
+    x = X.float().numpy()
+    top = np.abs(x).max(axis=1, initial=0.0).astype(np.float32)
+    s = np.where(top == 0, np.float32(1), np.maximum(top / np.float32(127), np.float32(2.0 ** -126))).astype(np.float32)
+    return np.rint(x / s[:, None]).astype(np.int8), s
+
+
+def _check_quant(X, Xd):
+    Q, s = sg.quantize_int8_rowwise(Xd)
+    assert sg.check() == sg.OK
+    q, want = _quant(X)
+    assert np.array_equal(s.cpu().numpy(), want)
+    assert np.array_equal(Q.cpu().numpy(), q)
+    assert Q.shape == X.shape and (X.shape[0] <= 1 or Q.stride(0) % 16 == 0)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+@pytest.mark.parametrize("cols", [1, 3, 8, 127, 256, 257, 1000, 1024, 1025, 4096, 8200, 16384, 33000])
+def test_codes_and_scales(cuda_device, dtype, cols):
+    X = normal(201, cols, (7, cols), dtype)
+    X[2] *= 1e-3
+    X[3] = 0
+    X[4, cols // 2] = 300.0
+    _check_quant(X, pitched(X.cuda()))
+
+
+@pytest.mark.parametrize("rows", [1, 2, 5, 4096])
+def test_row_counts_and_pitches(cuda_device, rows):
+    X = normal(202, rows, (rows, 200), BF)
+    _check_quant(X, pitched(X.cuda(), extra=3))
+
+
+def test_ties_and_scale_extremes(cuda_device):
+    """Quotients that are exact ties (scale 1: amax 127, values n + 0.5), scales in the
+    subnormal range and at its edge, the largest finite values, signs of zero."""
+    tie = torch.arange(-127, 127, dtype=torch.float32) + 0.5
+    tie = torch.cat([tie, torch.tensor([127.0, -127.0, 0.0, -0.0])])
+    rows = [tie, tie * 2.0 ** -100, tie * 2.0 ** -126, tie * 2.0 ** -140, tie * 2.0 ** 120, torch.full_like(tie, 1e-45)]
+    X = torch.stack(rows)
+    _check_quant(X, pitched(X.cuda()))
+
+
+def test_reciprocal_edges_of_the_scale(cuda_device):
+    """Scales over many significands, all-ones ones among them: the quotient is the
+    correctly rounded one for each."""
+    g = torch.Generator().manual_seed(6)
+    X = torch.randn(512, 96, generator=g) * torch.exp2(torch.randint(-60, 60, (512, 1), generator=g).float())
+    X[:, 0] = torch.exp2(torch.randint(-20, 20, (512,), generator=g).float()) * (2 - 2.0 ** -23) * 127
+    _check_quant(X, pitched(X.cuda()))
+
+
+def test_rows_with_nan_or_infinity_keep_it_in_the_scale(cuda_device):
+    X = normal(203, 0, (4, 300), BF)
+    X[1, 7], X[2, 250], X[3, 0], X[3, 299] = float("nan"), float("-inf"), float("inf"), float("nan")
+    _, s = sg.quantize_int8_rowwise(pitched(X.cuda()))
+    s = s.cpu()
+    assert s[0].isfinite() and s[1].isnan() and s[2] == float("inf") and s[3].isnan()
+
+
+def test_rows_without_elements_get_scale_one(cuda_device):
+    Q, s = sg.quantize_int8_rowwise(torch.zeros(3, 0, dtype=BF, device="cuda"))
+    assert Q.shape == (3, 0) and (s == 1).all()
+    Q, s = sg.quantize_int8_rowwise(torch.zeros(0, 32, dtype=BF, device="cuda"))
+    assert Q.shape == (0, 32) and s.shape == (0,)
+
+
+def test_codes_stay_inside_their_columns(cuda_device):
+    buf = torch.full((5, 64), 77, dtype=torch.int8, device="cuda")
+    X = normal(204, 0, (5, 33), BF)
+    sg.quantize_int8_rowwise(pitched(X.cuda()), Q=buf[:, :33])
+    assert sg.check() == sg.OK
+    assert (buf[:, 33:] == 77).all() and np.array_equal(buf[:, :33].cpu().numpy(), _quant(X)[0])
+
+
+# ---------------------------------------------------------------- products
+
+
+def _ref(a, sa, b, sb, bias, act):
+    """Value and slack: FP32 roundings of the sum's conversion, the two scales' product, their
+    product and the bias add."""
+    y = (a.double() @ b.double().T) * sa.double()[:, None] * sb.double()[None, :]
+    slack = y.abs() * (3.1 * U32)
+    if bias is not None:
+        y = y + bias.double()
+        slack = slack + y.abs() * U32
+    return act64(y, act), slack
+
+
+def _scales(seed, i, n):
+    return (normal(seed, i, (n,), F32).abs() + 0.1) * 0.02
+
+
+SHAPES = [(1, 16, 16), (1, 4096, 520), (3, 100, 1), (16, 1, 256), (31, 128, 257), (33, 129, 255), (64, 2048, 40),
+          (65, 127, 1000), (200, 512, 328), (257, 1000, 1003), (700, 4096, 264)]
+
+
+@pytest.mark.parametrize("M,K,N", SHAPES)
+@pytest.mark.parametrize("out,act,bias", [(BF, "none", None), (HF, "silu", BF), (F32, "gelu_tanh", F32), (F32, "none", HF)])
+def test_dense_product(cuda_device, M, K, N, out, act, bias):
+    a, b = codes(211, 0, (M, K)), codes(211, 1, (N, K))
+    sa, sb = _scales(211, 2, M), _scales(211, 3, N) / K ** 0.5
+    t = None if bias is None else normal(211, 4, (N,), bias, 0.5)
+    got = sg.gemm_int8_scaled(pitched(a.cuda()), sa.cuda(), pitched(b.cuda()), sb.cuda(),
+                              bias=None if t is None else t.cuda(), act=act, out_dtype=out)
+    assert sg.check() == sg.OK
+    ref, slack = _ref(a, sa, b, sb, t, act)
+    check_as(out, got.cpu(), ref, slack, act, f"{M}x{K}x{N}")
+
+
+def test_sums_are_exact_at_the_longest_k(cuda_device):
+    """K = 131071 codes of -128: every sum is 128 * 128 * K, just below 2^31; with signs
+    alternating by column the sums are +-that. Split along K, the pieces add as integers."""
+    K, N = 131071, 300
+    a = torch.full((2, K), -128, dtype=torch.int8)
+    a[1] = 127
+    b = torch.full((N, K), -128, dtype=torch.int8)
+    b[1::2] = 127
+    one = lambda n: torch.ones(n, device="cuda")
+    got = sg.gemm_int8_scaled(pitched(a.cuda()), one(2), pitched(b.cuda()), one(N), out_dtype=F32).cpu()
+    assert sg.check() == sg.OK
+    want = (a.double() @ b.double().T).float()
+    assert torch.equal(got, want)
+    with pytest.raises(sg.SmgemmError):
+        sg.gemm_int8_scaled(torch.zeros(1, 131072, dtype=torch.int8, device="cuda"), one(1),
+                            torch.zeros(16, 131072, dtype=torch.int8, device="cuda"), one(16))
+
+
+def test_no_inner_dimension(cuda_device):
+    z = torch.zeros(5, 0, dtype=torch.int8, device="cuda")
+    w = torch.zeros(40, 0, dtype=torch.int8, device="cuda")
+    bias = normal(212, 0, (40,), F32)
+    got = sg.gemm_int8_scaled(z, torch.ones(5, device="cuda"), w, torch.ones(40, device="cuda"), bias=bias.cuda(),
+                              act="silu", out_dtype=F32)
+    assert sg.check() == sg.OK
+    want = act64(bias.double(), "silu").expand(5, 40)
+    assert (got.cpu().double() - want).abs().max() <= 2 * U32 * want.abs().max()
+
+
+GROUPS = [([0, 3, 0, 1, 7, 0, 0, 2], 0, 3), ([31, 32, 33, 0, 64, 65], 2, 1), ([255, 257, 300], 1, 4), ([0, 0], 3, 3)]
+
+
+@pytest.mark.parametrize("counts,head,tail", GROUPS)
+@pytest.mark.parametrize("K,N", [(128, 256), (333, 515), (4096, 40)])
+@pytest.mark.parametrize("out,act,bias", [(BF, "none", None), (F32, "silu", BF)])
+def test_ragged_product(cuda_device, counts, head, tail, K, N, out, act, bias):
+    E, T = len(counts), head + sum(counts) + tail
+    a, b = codes(213, 0, (T, K)), codes(213, 1, (E, N, K))
+    sa, sb = _scales(213, 2, T), _scales(213, 3, E * N).view(E, N) / K ** 0.5
+    t = None if bias is None else normal(213, 4, (E, N), bias, 0.5)
+    off = offsets_of(counts, head)
+    C = pitched(torch.full((T, N), 7.0, dtype=out).cuda())
+    got = sg.gemm_int8_ragged(pitched(a.cuda()), sa.cuda(), pitched(b.cuda()), sb.cuda(), off.cuda(),
+                              bias=None if t is None else t.cuda(), act=act, out=C).cpu()
+    assert sg.check() == sg.OK
+    for e in range(E):
+        r = slice(int(off[e]), int(off[e + 1]))
+        ref, slack = _ref(a[r], sa[r], b[e], sb[e], None if t is None else t[e], act)
+        check_as(out, got[r], ref, slack, act, f"expert {e}")
+    assert (got[:head] == 7.0).all() and (got[T - tail:] == 7.0).all()
+
+
+def test_quantised_expert_layer_together(cuda_device):
+    """Serving an expert FFN in int8: quantise tokens, up product with SiLU, quantise its
+    BF16 result, down product - against the same chain in 64 bits on the same codes and
+    scales; the second product's inputs are the first's outputs read back."""
+    counts, K, H = [4, 0, 40, 1], 320, 512
+    E, T, off = len(counts), sum(counts), offsets_of(counts)
+    X = normal(214, 0, (T, K), BF)
+    W1, W2 = normal(214, 1, (E * H, K), BF, K ** -0.5), normal(214, 2, (E * K, H), BF, H ** -0.5)
+    o = off.cuda()
+    w1, s1 = sg.quantize_int8_rowwise(W1.cuda())
+    w2, s2 = sg.quantize_int8_rowwise(W2.cuda())
+    w1, s1, w2, s2 = w1.view(E, H, K), s1.view(E, H), w2.view(E, K, H), s2.view(E, K)
+    xq, sx = sg.quantize_int8_rowwise(X.cuda())
+    h = sg.gemm_int8_ragged(xq, sx, w1, s1, o, act="silu")
+    hq, sh = sg.quantize_int8_rowwise(h)
+    y = sg.gemm_int8_ragged(hq, sh, w2, s2, o, out_dtype=F32)
+    assert sg.check() == sg.OK
+    for e in range(E):
+        r = slice(int(off[e]), int(off[e + 1]))
+        ref, slack = _ref(xq[r].cpu(), sx[r].cpu(), w1[e].cpu(), s1[e].cpu(), None, "silu")
+        check_as(BF, h[r].cpu(), ref, slack, "silu", "up")
+        ref, slack = _ref(hq[r].cpu(), sh[r].cpu(), w2[e].cpu(), s2[e].cpu(), None, "none")
+        check_as(F32, y[r].cpu(), ref, slack, what="down")
+    # the layer in BF16 for scale: 8-bit rounding of both operands, 1/254 of each row's maximum per element
+    ref = torch.cat([(act64(X[int(off[e]):int(off[e + 1])].double() @ W1.view(E, H, K)[e].double().T, "silu")
+                      @ W2.view(E, K, H)[e].double().T) for e in range(E)])
+    assert (y.cpu().double() - ref).norm() <= 0.05 * ref.norm()
+
+
+def test_captured_decode_step_replays(cuda_device):
+    """Quantise + product captured once, replayed on new tokens (tiles cut along K)."""
+    X = torch.zeros(3, 4096, dtype=BF, device="cuda")
+    w, sw = codes(215, 0, (1024, 4096)).cuda(), _scales(215, 1, 1024).cuda()
+    out = torch.zeros(3, 1024, dtype=BF, device="cuda")
+
+    def step():
+        q, s = sg.quantize_int8_rowwise(X)
+        sg.gemm_int8_scaled(q, s, w, sw, out=out)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(3):
+        X.copy_(normal(216, i, (3, 4096), BF))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        step()
+        assert sg.check() == sg.OK
+        assert torch.equal(got, out)
+
+
+def test_refusals(cuda_device):
+    z = lambda *s, dt=torch.int8: torch.zeros(*s, dtype=dt, device="cuda")
+    f = lambda *s: torch.ones(*s, device="cuda")
+    with pytest.raises(ValueError):
+        sg.quantize_int8_rowwise(z(4, 16, dt=torch.float64))
+    with pytest.raises(ValueError):
+        sg.quantize_int8_rowwise(z(16, 4, dt=BF).t())
+    with pytest.raises(ValueError):
+        sg.quantize_int8_rowwise(torch.zeros(4, 16))
+    with pytest.raises(ValueError):
+        sg.quantize_int8_rowwise(z(4, 16, dt=BF), Q=z(4, 16, dt=torch.uint8))
+    with pytest.raises(sg.SmgemmError):
+        sg.quantize_int8_rowwise(z(4, 17, dt=BF))                        # 34-byte row pitch
+    with pytest.raises(ValueError):
+        sg.gemm_int8_scaled(z(4, 16), f(4), z(8, 32), f(8))
+    with pytest.raises(ValueError):
+        sg.gemm_int8_scaled(z(4, 16), f(5), z(8, 16), f(8))
+    with pytest.raises(ValueError):
+        sg.gemm_int8_scaled(z(4, 16, dt=torch.uint8), f(4), z(8, 16), f(8))
+    with pytest.raises(sg.SmgemmError):
+        sg.gemm_int8_scaled(z(4, 24), f(4), z(8, 24), f(8))              # 24-byte row pitch
+    with pytest.raises(sg.SmgemmError):
+        sg.gemm_int8_scaled(z(4, 16), f(4), z(8, 16), f(8), workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        sg.gemm_int8_ragged(z(4, 16), f(4), z(2, 16, 8).mT, f(2, 8), torch.zeros(3, dtype=torch.int32, device="cuda"))
+    assert sg.check() == sg.OK

@@ -1,0 +1,425 @@
+"""Products of rows sorted by expert (gemm_bf16_ragged, gemm_bf16_ragged_wgrad): device
+offsets, every layout, type and epilogue, experts without rows, rows of no expert, odd
+sizes, against plain products in 64 bits expert by expert."""
+import pytest
+import torch
+
+import sm_gemm_b200 as sg
+from _ragged import U32, act64, check_as, normal, offsets_of, pitched, products64
+
+pytestmark = pytest.mark.gpu
+
+BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
+
+# (counts per expert, rows before the first, rows after the last)
+GROUPS = {
+    "one row each": ([1] * 5, 0, 0),
+    "decode, idle experts": ([0, 3, 0, 1, 7, 0, 0, 2], 0, 3),
+    "32-row edges": ([31, 32, 33, 0, 64, 65], 2, 1),
+    "tile edges": ([255, 256, 257, 300, 1], 0, 0),
+    "one long": ([700], 5, 9),
+    "all idle": ([0, 0, 0], 4, 4),
+    "40 experts": ([(7 * i) % 23 for i in range(40)], 0, 0),
+}
+
+
+def _case(seed, groups, K, N, dtype, layout):
+    counts, head, tail = GROUPS[groups]
+    E, T = len(counts), head + sum(counts) + tail
+    A = normal(seed, 0, (T, K), dtype)
+    W = normal(seed, 1, (E, K, N), dtype, K ** -0.5)
+    Wd = pitched(W.cuda()) if layout == "row" else pitched(W.mT.contiguous().cuda()).mT
+    return A, W, pitched(A.cuda()), Wd, offsets_of(counts, head)
+
+
+def _forward64(A, W, off, bias=None, act="none"):
+    """Reference, slack and the mask of rows that some expert has."""
+    T, N = A.shape[0], W.shape[2]
+    ref, slack = torch.zeros(T, N, dtype=torch.float64), torch.zeros(T, N, dtype=torch.float64)
+    for e in range(W.shape[0]):
+        r = slice(int(off[e]), int(off[e + 1]))
+        y, s = products64(A[r], W[e])
+        if bias is not None:
+            y = y + bias[e].double()
+            s = s + y.abs() * U32
+        ref[r], slack[r] = act64(y, act), s
+    mine = torch.zeros(T, dtype=torch.bool)
+    mine[int(off[0]):int(off[-1])] = True
+    return ref, slack, mine
+
+
+@pytest.mark.parametrize("groups", list(GROUPS))
+@pytest.mark.parametrize("layout", ["row", "col"])
+@pytest.mark.parametrize("dtype,out,act,bias", [(BF, BF, "none", None), (HF, HF, "silu", HF), (BF, F32, "gelu_tanh", F32),
+                                                (HF, BF, "gelu_tanh", BF)])
+def test_forward(cuda_device, groups, layout, dtype, out, act, bias):
+    K, N = 200, 328
+    A, W, Ad, Wd, off = _case(101, groups, K, N, dtype, layout)
+    b = None if bias is None else normal(101, 2, (W.shape[0], N), bias, 0.5)
+    C = pitched(torch.full((A.shape[0], N), 7.0, dtype=out).cuda())
+    got = sg.gemm_bf16_ragged(Ad, Wd, off.cuda(), bias=None if b is None else b.cuda(), act=act, out=C)
+    assert sg.check() == sg.OK and got is C
+    ref, slack, mine = _forward64(A, W, off, b, act)
+    got = got.cpu()
+    assert (got[~mine] == 7.0).all(), "rows of no expert were written"
+    check_as(out, got[mine], ref[mine], slack[mine], act, groups)
+
+
+@pytest.mark.parametrize("K,N", [(1, 1), (7, 5), (63, 255), (64, 256), (65, 257), (513, 1003), (2048, 40)])
+@pytest.mark.parametrize("layout", ["row", "col"])
+def test_forward_odd_sizes(cuda_device, K, N, layout):
+    A, W, Ad, Wd, off = _case(102, "32-row edges", K, N, BF, layout)
+    got = sg.gemm_bf16_ragged(Ad, Wd, off.cuda(), out_dtype=F32)
+    assert sg.check() == sg.OK
+    ref, slack, mine = _forward64(A, W, off)
+    check_as(F32, got.cpu()[mine], ref[mine], slack[mine], what=f"{K}x{N}")
+
+
+@pytest.mark.parametrize("groups", ["decode, idle experts", "tile edges"])
+def test_no_inner_dimension_writes_the_activated_bias(cuda_device, groups):
+    counts, head, tail = GROUPS[groups]
+    E, T, N = len(counts), head + sum(counts) + tail, 40
+    bias = normal(103, 0, (E, N), F32)
+    C = torch.full((T, N), 7.0, device="cuda")
+    sg.gemm_bf16_ragged(torch.zeros(T, 0, dtype=BF, device="cuda"), torch.zeros(E, 0, N, dtype=BF, device="cuda"),
+                        offsets_of(counts, head).cuda(), bias=bias.cuda(), act="silu", out=C)
+    assert sg.check() == sg.OK
+    e = torch.repeat_interleave(torch.arange(E), torch.tensor(counts))
+    want = torch.full((T, N), 7.0, dtype=torch.float64)
+    want[head:head + sum(counts)] = act64(bias.double(), "silu")[e]
+    assert (C.cpu().double() - want).abs().max() <= 2 * U32 * want.abs().max()
+
+
+@pytest.mark.parametrize("K", [4096, 1000])
+@pytest.mark.parametrize("counts", [[5, 0, 17], [300, 20]])
+def test_split_along_k_is_exact_on_integers_and_repeats(cuda_device, K, counts):
+    """Few tiles and a long K: the tiles are cut along K. Small integers make every partial
+    sum exact, so any order gives the same bits; random values must repeat bit for bit."""
+    T, N = sum(counts), 520
+    A = torch.randint(-3, 4, (T, K), generator=torch.Generator().manual_seed(1)).to(BF)
+    W = torch.randint(-3, 4, (len(counts), K, N), generator=torch.Generator().manual_seed(2)).to(BF)
+    off = offsets_of(counts)
+    got = sg.gemm_bf16_ragged(A.cuda(), W.cuda(), off.cuda(), out_dtype=F32).cpu()
+    assert sg.check() == sg.OK
+    ref, _, mine = _forward64(A, W, off)
+    assert torch.equal(got.double()[mine], ref[mine])
+    A, W = normal(104, 0, (T, K), BF).cuda(), normal(104, 1, (len(counts), K, N), BF).cuda()
+    first = sg.gemm_bf16_ragged(A, W, off.cuda(), out_dtype=F32).clone()
+    for _ in range(3):
+        assert torch.equal(sg.gemm_bf16_ragged(A, W, off.cuda(), out_dtype=F32), first)
+
+
+def test_offsets_that_are_no_partition_stay_inside_the_output(cuda_device):
+    """Offsets outside 0..T or decreasing are clamped: rows go to the experts of the clamped
+    bounds and nothing outside the output's rows is touched."""
+    T, K, N = 100, 64, 72
+    A, W = normal(105, 0, (T, K), BF), normal(105, 1, (4, K, N), BF, 0.1)
+    buf = torch.full((T + 64, N), 7.0, dtype=BF, device="cuda")
+    off = torch.tensor([-5, 40, 10, 70, 1 << 30], dtype=torch.int32)
+    sg.gemm_bf16_ragged(A.cuda(), W.cuda(), off.cuda(), out=buf[32:32 + T])
+    assert sg.check() == sg.OK
+    got = buf.cpu()
+    assert (got[:32] == 7.0).all() and (got[32 + T:] == 7.0).all()
+    ref, slack, mine = _forward64(A, W, torch.tensor([0, 40, 40, 70, 100]))
+    check_as(BF, got[32:32 + T], ref, slack)
+
+
+def test_rows_of_other_experts_do_not_leak(cuda_device):
+    """NaN and infinities in rows of no expert and in another expert's rows and weights stay
+    there, in the product and in the weight gradient (whose row blocks are shared)."""
+    counts, head, tail = [70, 5, 0, 90], 3, 6
+    E, T, K, N = 4, 3 + 165 + 6, 96, 136
+    A, D = normal(106, 0, (T, K), BF), normal(106, 1, (T, N), BF)
+    W = normal(106, 2, (E, K, N), BF, 0.1)
+    off = offsets_of(counts, head)
+    for t in (A, D):
+        t[:head] = float("nan")
+        t[-tail:] = float("inf")
+        t[int(off[1]):int(off[2])] = float("nan")
+    W[2] = float("nan")
+    C = sg.gemm_bf16_ragged(A.cuda(), W.cuda(), off.cuda()).cpu()
+    db = torch.empty(E, N, device="cuda")
+    dW = sg.gemm_bf16_ragged_wgrad(A.cuda(), D.cuda(), off.cuda(), dbias=db).cpu()
+    assert sg.check() == sg.OK
+    assert C[int(off[1]):int(off[2])].isnan().all() and dW[1].isnan().all() and db[1].isnan().all()
+    for e in (0, 3):
+        r = slice(int(off[e]), int(off[e + 1]))
+        y, s = products64(A[r], W[e])
+        check_as(BF, C[r], y, s, what=f"C, expert {e}")
+        y, s = products64(A[r].T, D[r])
+        check_as(BF, dW[e], y, s, what=f"dW, expert {e}")
+        assert db[e].isfinite().all()
+    assert (dW[2] == 0).all() and (db[2] == 0).all()
+
+
+@pytest.mark.parametrize("groups", list(GROUPS))
+@pytest.mark.parametrize("dtype,out,K,N", [(BF, BF, 136, 264), (HF, F32, 300, 200), (HF, HF, 257, 1), (BF, F32, 64, 515)])
+def test_weight_and_bias_gradients(cuda_device, groups, dtype, out, K, N):
+    counts, head, tail = GROUPS[groups]
+    E, T = len(counts), head + sum(counts) + tail
+    A, D = normal(107, 0, (T, K), dtype), normal(107, 1, (T, N), dtype)
+    off = offsets_of(counts, head)
+    C = pitched(torch.full((E, K, N), 7.0, dtype=out).cuda())
+    db = torch.full((E, N), 7.0, device="cuda")
+    got = sg.gemm_bf16_ragged_wgrad(pitched(A.cuda()), pitched(D.cuda()), off.cuda(), out=C, dbias=db)
+    assert sg.check() == sg.OK and got is C
+    got, db = got.cpu(), db.cpu()
+    for e in range(E):
+        r = slice(int(off[e]), int(off[e + 1]))
+        ref, slack = products64(A[r].T, D[r])
+        check_as(out, got[e], ref, slack, what=f"dW[{e}]")
+        d = D[r].double()
+        check_as(F32, db[e], d.sum(0), d.abs().sum(0) * U32 * (counts[e] + 8), what=f"dbias[{e}]")
+
+
+def test_weight_gradient_split_along_rows(cuda_device):
+    """Two experts with many rows and few tiles: the last wave's tiles are cut along the rows."""
+    counts = [1500, 2011]
+    T, K, N = sum(counts), 264, 520
+    A = torch.randint(-2, 3, (T, K), generator=torch.Generator().manual_seed(3)).to(BF)
+    D = torch.randint(-2, 3, (T, N), generator=torch.Generator().manual_seed(4)).to(BF)
+    off = offsets_of(counts)
+    got = sg.gemm_bf16_ragged_wgrad(A.cuda(), D.cuda(), off.cuda(), out_dtype=F32).cpu()
+    assert sg.check() == sg.OK
+    for e in range(2):
+        r = slice(int(off[e]), int(off[e + 1]))
+        assert torch.equal(got[e].double(), A[r].double().T @ D[r].double())
+
+
+def test_weight_gradient_of_an_empty_batch_is_zero(cuda_device):
+    z = lambda *s: torch.zeros(*s, dtype=BF, device="cuda")
+    db = torch.full((3, 24), 7.0, device="cuda")
+    got = sg.gemm_bf16_ragged_wgrad(z(0, 40), z(0, 24), torch.zeros(4, dtype=torch.int32, device="cuda"), dbias=db)
+    assert sg.check() == sg.OK and got.shape == (3, 40, 24)
+    assert (got == 0).all() and (db == 0).all()
+
+
+def test_no_rows_no_experts_no_columns(cuda_device):
+    z = lambda *s: torch.zeros(*s, dtype=BF, device="cuda")
+    o = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")
+    assert sg.gemm_bf16_ragged(z(0, 16), z(2, 16, 8), o(3)).shape == (0, 8)
+    out = torch.full((4, 8), 7.0, dtype=BF, device="cuda")
+    sg.gemm_bf16_ragged(z(4, 16), z(0, 16, 8), o(1), out=out)
+    assert (out == 7.0).all()
+    assert sg.gemm_bf16_ragged(z(4, 16), z(2, 16, 0), o(3)).shape == (4, 0)
+    assert sg.gemm_bf16_ragged_wgrad(z(4, 16), z(4, 8), o(1)).shape == (0, 16, 8)
+    assert sg.check() == sg.OK
+
+
+def test_many_experts(cuda_device):
+    """1024 experts, the most a call takes, most of them idle."""
+    E, K, N = 1024, 64, 32
+    counts = [(i % 7 == 0) * (i % 5) for i in range(E)]
+    T = sum(counts)
+    A, W, off = normal(108, 0, (T, K), BF), normal(108, 1, (E, K, N), BF, 0.1), offsets_of(counts)
+    got = sg.gemm_bf16_ragged(A.cuda(), W.cuda(), off.cuda())
+    dW = sg.gemm_bf16_ragged_wgrad(A.cuda(), got, off.cuda())
+    assert sg.check() == sg.OK
+    ref, slack, _ = _forward64(A, W, off)
+    check_as(BF, got.cpu(), ref, slack)
+    got = got.cpu()
+    for e in range(E):
+        r = slice(int(off[e]), int(off[e + 1]))
+        y, s = products64(A[r].T, got[r])
+        check_as(BF, dW[e].cpu(), y, s, what=f"dW[{e}]")
+
+
+def test_output_rows_past_32_bit_offsets(cuda_device):
+    """Rows whose first element lies more than 2^31 elements into the output's buffer."""
+    T, K, N, ld = 60000, 64, 40, 40000
+    buf = torch.empty(T * ld, dtype=BF, device="cuda").view(T, ld)
+    A, W = normal(109, 0, (T, K), BF), normal(109, 1, (2, K, N), BF, 0.1)
+    off = torch.tensor([0, 30001, T], dtype=torch.int32)
+    sg.gemm_bf16_ragged(A.cuda(), W.cuda(), off.cuda(), out=buf[:, :N])
+    assert sg.check() == sg.OK
+    got = buf[:, :N].cpu()
+    ref, slack, _ = _forward64(A, W, off)
+    check_as(BF, got, ref, slack)
+
+
+def test_moe_layer_forward_and_backward_together(cuda_device):
+    """An expert FFN layer trained for one step: up product, SiLU, down product, and from the
+    output's gradient dX, both weight gradients and the down bias's gradient, against 64-bit
+    autograd of the formulas on the same BF16 inputs. Every product rounds its result to
+    BF16 once (2^-8 relative); errors pass through at most two more products, so outputs
+    are held to 4 of those in the 2-norm."""
+    torch.manual_seed(5)
+    counts, K, H = [37, 0, 130, 9, 300], 256, 512
+    E, T = len(counts), sum(counts)
+    off = offsets_of(counts)
+    X, W1, W2 = (torch.randn(T, K).to(BF), (torch.randn(E, K, H) / K ** 0.5).to(BF), (torch.randn(E, H, K) / H ** 0.5).to(BF))
+    b2, dY = torch.randn(E, K).mul(0.1).to(BF), torch.randn(T, K).to(BF)
+    x, w1, w2, b = (t.double().requires_grad_() for t in (X, W1, W2, b2))
+    y = []
+    for e in range(E):
+        r = slice(int(off[e]), int(off[e + 1]))
+        h = x[r] @ w1[e]
+        y.append((h * torch.sigmoid(h)) @ w2[e] + b[e])
+    y = torch.cat(y)
+    y.backward(dY.double())
+    o = off.cuda()
+    Xd, W1d, W2d, dYd = X.cuda(), W1.cuda(), W2.cuda(), dY.cuda()
+    Z = sg.gemm_bf16_ragged(Xd, W1d, o)
+    Hd = (Z.float() * torch.sigmoid(Z.float())).to(BF)
+    assert torch.equal(sg.gemm_bf16_ragged(Xd, W1d, o, act="silu").isfinite().all(), torch.tensor(True, device="cuda"))
+    Y = sg.gemm_bf16_ragged(Hd, W2d, o, bias=b2.cuda())
+    dH = sg.gemm_bf16_ragged(dYd, W2d.mT, o)
+    db2 = torch.empty(E, K, device="cuda")
+    dW2 = sg.gemm_bf16_ragged_wgrad(Hd, dYd, o, dbias=db2)
+    s = torch.sigmoid(Z.float())
+    dZ = (dH.float() * s * (1 + Z.float() * (1 - s))).to(BF)
+    dX = sg.gemm_bf16_ragged(dZ, W1d.mT, o)
+    dW1 = sg.gemm_bf16_ragged_wgrad(Xd, dZ, o)
+    assert sg.check() == sg.OK
+    for name, got, ref in (("Y", Y, y.detach()), ("dX", dX, x.grad), ("dW1", dW1, w1.grad), ("dW2", dW2, w2.grad),
+                           ("db2", db2, b.grad)):
+        err = (got.cpu().double() - ref).norm() / ref.norm()
+        assert err <= 4 * 2.0 ** -8, f"{name}: {err}"
+
+
+def test_gradients_match_differences(cuda_device):
+    """dX and dW against central differences of sum(C * D) on an FP32-output product of
+    BF16 values whose steps are exact (the function is linear in each operand, so the
+    difference quotient has no truncation error)."""
+    counts, K, N = [3, 0, 40], 24, 16
+    T, off = sum(counts), offsets_of(counts).cuda()
+    A, W = normal(110, 0, (T, K), BF), normal(110, 1, (3, K, N), BF)
+    D = normal(110, 2, (T, N), BF)
+    A, W, D = A.cuda(), W.cuda(), D.cuda()
+    dX = sg.gemm_bf16_ragged(D, W.mT, off, out_dtype=F32)
+    dW = sg.gemm_bf16_ragged_wgrad(A, D, off, out_dtype=F32)
+
+    def loss(a, w):
+        return (sg.gemm_bf16_ragged(a, w, off, out_dtype=F32).double() * D.double()).sum()
+
+    for t, k in ((0, 0), (2, 23), (20, 7), (42, 11)):
+        lo, hi = A.clone(), A.clone()
+        lo[t, k], hi[t, k] = -2.0, 2.0
+        want = (loss(hi, W) - loss(lo, W)) / 4.0
+        assert abs(want - dX[t, k].double()) <= 1e-3, (t, k)
+    for e, k, n in ((0, 0, 0), (2, 23, 15), (2, 5, 3), (1, 4, 4)):
+        lo, hi = W.clone(), W.clone()
+        lo[e, k, n], hi[e, k, n] = -2.0, 2.0
+        want = (loss(A, hi) - loss(A, lo)) / 4.0
+        assert abs(want - dW[e, k, n].double()) <= 1e-3, (e, k, n)
+
+
+def test_captured_calls_replay_with_other_offsets(cuda_device):
+    """One captured forward and weight gradient, replayed with other inputs and offsets."""
+    E, T, K, N = 6, 200, 512, 264
+    A, W = normal(111, 0, (T, K), BF).cuda(), normal(111, 1, (E, K, N), BF, 0.05).cuda()
+    D = normal(111, 2, (T, N), BF).cuda()
+    off = offsets_of([50, 0, 20, 30, 0, 100]).cuda()
+    C, dW, db = torch.zeros(T, N, dtype=BF, device="cuda"), torch.zeros(E, K, N, device="cuda"), torch.zeros(E, N, device="cuda")
+
+    def step():
+        sg.gemm_bf16_ragged(A, W, off, act="silu", out=C)
+        sg.gemm_bf16_ragged_wgrad(A, D, off, out=dW, dbias=db)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed, counts in ((1, [50, 0, 20, 30, 0, 100]), (2, [0, 0, 200, 0, 0, 0]), (3, [1, 2, 3, 4, 5, 6]), (4, [0] * 6)):
+        A.copy_(normal(112, seed, (T, K), BF))
+        off.copy_(offsets_of(counts))
+        for t in (C, dW, db):
+            t.fill_(5.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert sg.check() == sg.OK
+        got = [t.clone() for t in (C, dW, db)]
+        for t in (C, dW, db):
+            t.fill_(5.0)
+        step()
+        for g, w in zip(got, (C, dW, db)):
+            assert torch.equal(g, w), counts
+
+
+def test_two_graphs_and_eager_calls_side_by_side(cuda_device):
+    """Two captured graphs replayed on two streams while a third stream runs the same call
+    eagerly: each has its own workspace (every tile here is cut along K)."""
+    K, N = 8192, 512
+    ins = [(normal(113, 2 * i, (40, K), BF).cuda(), normal(113, 2 * i + 1, (2, K, N), BF, 0.02).cuda()) for i in range(3)]
+    off = offsets_of([25, 15]).cuda()
+    outs = [torch.zeros(40, N, device="cuda") for _ in range(3)]
+    want = [sg.gemm_bf16_ragged(a, w, off, out_dtype=F32) for a, w in ins]
+    torch.cuda.synchronize()
+    graphs = []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(4):
+                sg.gemm_bf16_ragged(*ins[i], off, out=outs[i])
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(20):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+        for _ in range(4):
+            sg.gemm_bf16_ragged(*ins[2], off, out=outs[2], stream=streams[2])
+    torch.cuda.synchronize()
+    assert sg.check() == sg.OK
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
+
+
+def test_outputs_of_a_call_on_another_stream(cuda_device):
+    """A call given a stream allocates for that stream: its output is not memory that the
+    current stream's queued work still uses."""
+    A, W = normal(114, 0, (64, 512), BF).cuda(), normal(114, 1, (2, 512, 256), BF, 0.05).cuda()
+    off = offsets_of([30, 34]).cuda()
+    want = sg.gemm_bf16_ragged(A, W, off)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(20):
+        busy = [torch.full((64, 256), 3.0, dtype=BF, device="cuda") for _ in range(4)]
+        torch.cuda._sleep(200000)
+        for b in busy:
+            b.add_(1)
+        del busy
+        got = sg.gemm_bf16_ragged(A, W, off, stream=s)
+        s.synchronize()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+
+
+def test_refusals(cuda_device):
+    z = lambda *s, dt=BF: torch.zeros(*s, dtype=dt, device="cuda")
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        sg.gemm_bf16_ragged(z(4, 16), z(2, 24, 8), off)                  # K differs
+    with pytest.raises(ValueError):
+        sg.gemm_bf16_ragged(z(4, 16), z(2, 16, 8, dt=HF), off)           # types differ
+    with pytest.raises(ValueError):
+        sg.gemm_bf16_ragged(z(4, 16), z(2, 16, 8), off.long())           # offsets not int32
+    with pytest.raises(ValueError):
+        sg.gemm_bf16_ragged(z(4, 16), z(3, 16, 8), off)                  # E + 1 offsets
+    with pytest.raises(ValueError):
+        sg.gemm_bf16_ragged(z(4, 16), z(2, 16, 8), off.cpu())            # offsets on the host
+    with pytest.raises(ValueError):
+        sg.gemm_bf16_ragged(z(16, 4).t(), z(2, 16, 8), off)              # A column-major
+    with pytest.raises(ValueError):
+        sg.gemm_bf16_ragged(z(4, 16), z(2, 16, 8), off, bias=z(8))       # bias not [E, N]
+    with pytest.raises(ValueError):
+        sg.gemm_bf16_ragged(z(4, 16), z(2, 16, 8), off, act="relu")
+    with pytest.raises(sg.SmgemmError):
+        sg.gemm_bf16_ragged(z(4, 16), z(1, 16, 8).expand(2, 16, 8), off)  # matrices overlap
+    with pytest.raises(sg.SmgemmError):
+        sg.gemm_bf16_ragged(z(4, 15), z(2, 15, 8), off)                  # 30-byte row pitch
+    with pytest.raises(sg.SmgemmError):
+        sg.gemm_bf16_ragged(z(4, 16), z(1025, 16, 8), torch.zeros(1026, dtype=torch.int32, device="cuda"))
+    with pytest.raises(sg.SmgemmError):
+        sg.gemm_bf16_ragged(z(4, 16), z(2, 16, 8), off, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        sg.gemm_bf16_ragged_wgrad(z(4, 16), z(5, 8), off)                # rows differ
+    with pytest.raises(ValueError):
+        sg.gemm_bf16_ragged_wgrad(z(4, 16), z(4, 8), off, out=z(2, 8, 16).mT)
+    with pytest.raises(ValueError):
+        sg.gemm_bf16_ragged_wgrad(z(4, 16), z(4, 8), off, dbias=z(2, 8))  # dbias not float32
+    assert sg.check() == sg.OK

@@ -1,0 +1,117 @@
+"""Argument checks of the int8 and ragged products, at the C ABI (fake device addresses:
+every refusal comes before any CUDA call) and in the binding's layout helpers."""
+import pytest
+import torch
+
+import sm_gemm_b200 as sg
+
+FAKE = 0x7F0000001000
+needs_cpu = pytest.mark.skipif(torch.cuda.is_available(), reason="fake-pointer tests run only where no GPU can be reached")
+
+
+def _ragged(E=2, T=8, N=64, K=64, off=FAKE, A=FAKE, ab=sg.BF16, lda=None, B=FAKE, lb=sg.ROW_MAJOR, ldb=None, sB=None,
+            bias=None, bdt=sg.F32, act=0, Cp=FAKE, cdt=sg.BF16, ldc=None, ws=FAKE, wsb=1 << 40):
+    ldb = ldb if ldb is not None else (N if lb == sg.ROW_MAJOR else K)
+    sB = sB if sB is not None else N * K
+    return sg.lib().gemm_bf16_ragged(E, T, N, K, off, A, ab, lda if lda is not None else K, B, lb, ldb, sB, bias, bdt, act,
+                                     Cp, cdt, ldc if ldc is not None else N, ws, wsb, None)
+
+
+@needs_cpu
+def test_ragged_refusals():
+    assert _ragged(E=-1) == sg.ERR_INVALID_ARG
+    assert _ragged(T=-1) == sg.ERR_INVALID_ARG
+    assert _ragged(N=1 << 31) == sg.ERR_INVALID_ARG
+    assert _ragged(E=1025) == sg.ERR_UNSUPPORTED
+    assert _ragged(off=None) == sg.ERR_INVALID_ARG
+    assert _ragged(off=FAKE + 2) == sg.ERR_ALIGNMENT
+    assert _ragged(ab=sg.F32) == sg.ERR_UNSUPPORTED
+    assert _ragged(A=None) == sg.ERR_INVALID_ARG
+    assert _ragged(A=FAKE + 8) == sg.ERR_ALIGNMENT
+    assert _ragged(lda=63) == sg.ERR_INVALID_ARG
+    assert _ragged(lda=65) == sg.ERR_ALIGNMENT
+    assert _ragged(ldb=60) == sg.ERR_INVALID_ARG
+    assert _ragged(lb=2) == sg.ERR_INVALID_ARG
+    assert _ragged(sB=0) == sg.ERR_INVALID_ARG
+    assert _ragged(sB=64 * 64 - 8) == sg.ERR_INVALID_ARG
+    assert _ragged(sB=64 * 64 + 4) == sg.ERR_ALIGNMENT
+    assert _ragged(act=3) == sg.ERR_INVALID_ARG
+    assert _ragged(cdt=sg.E4M3) == sg.ERR_INVALID_ARG
+    assert _ragged(Cp=None) == sg.ERR_INVALID_ARG
+    assert _ragged(ldc=60) == sg.ERR_INVALID_ARG
+    assert _ragged(ldc=68) == sg.ERR_ALIGNMENT
+    assert _ragged(bias=FAKE + 2, bdt=sg.F32) == sg.ERR_ALIGNMENT
+    assert _ragged() == sg.ERR_CUDA                      # everything in order: no device here
+    for none in (dict(E=0), dict(T=0), dict(N=0)):       # nothing to do
+        assert _ragged(**none) == sg.OK
+
+
+def _int8(M=8, N=64, K=64, A=FAKE, lda=None, sa=FAKE, B=FAKE, ldb=None, sb=FAKE, Cp=FAKE, ldc=None):
+    return sg.lib().gemm_int8_scaled(M, N, K, A, lda if lda is not None else K, sa, B, ldb if ldb is not None else K, sb, None, 0,
+                                     0, Cp, sg.BF16, ldc if ldc is not None else N, FAKE, 1 << 40, None)
+
+
+@needs_cpu
+def test_int8_refusals():
+    assert _int8(M=-1) == sg.ERR_INVALID_ARG
+    assert _int8(K=131072) == sg.ERR_UNSUPPORTED
+    assert _int8(lda=72) == sg.ERR_ALIGNMENT
+    assert _int8(ldb=48) == sg.ERR_INVALID_ARG
+    assert _int8(sa=None) == sg.ERR_INVALID_ARG
+    assert _int8(sb=FAKE + 2) == sg.ERR_ALIGNMENT
+    assert _int8(B=FAKE + 4) == sg.ERR_ALIGNMENT
+    assert _int8() == sg.ERR_CUDA
+    assert _int8(M=0) == sg.OK
+
+
+@needs_cpu
+def test_quantiser_refusals():
+    def q(X=FAKE, dt=sg.BF16, rows=4, cols=64, ldx=64, Q=FAKE, ldq=64, S=FAKE):
+        return sg.lib().quantize_int8_rowwise(X, dt, rows, cols, ldx, Q, ldq, S, None)
+    assert q(rows=-1) == sg.ERR_INVALID_ARG
+    assert q(dt=sg.E4M3) == sg.ERR_UNSUPPORTED
+    assert q(ldx=63) == sg.ERR_INVALID_ARG
+    assert q(ldx=68) == sg.ERR_ALIGNMENT
+    assert q(ldq=72) == sg.ERR_ALIGNMENT
+    assert q(S=FAKE + 1) == sg.ERR_ALIGNMENT
+    assert q(Q=None) == sg.ERR_INVALID_ARG
+    assert q() == sg.ERR_CUDA
+    assert q(rows=0) == sg.OK
+
+
+@needs_cpu
+def test_weight_gradient_refusals():
+    def w(E=2, T=8, N=64, K=64, off=FAKE, A=FAKE, ab=sg.BF16, lda=64, D=FAKE, ldd=64, dB=FAKE, cdt=sg.F32, ldc=64, sC=4096,
+          db=None):
+        return sg.lib().gemm_bf16_ragged_wgrad(E, T, N, K, off, A, ab, lda, D, ldd, dB, cdt, ldc, sC, db, FAKE, 1 << 40, None)
+    assert w(E=2000) == sg.ERR_UNSUPPORTED
+    assert w(ab=sg.F32) == sg.ERR_UNSUPPORTED
+    assert w(D=None) == sg.ERR_INVALID_ARG
+    assert w(ldd=66) == sg.ERR_ALIGNMENT
+    assert w(sC=4000) == sg.ERR_INVALID_ARG
+    assert w(sC=4097) == sg.ERR_ALIGNMENT
+    assert w(db=FAKE + 2) == sg.ERR_ALIGNMENT
+    assert w(cdt=9) == sg.ERR_INVALID_ARG
+    assert w() == sg.ERR_CUDA
+    assert w(E=0) == sg.OK
+
+
+def test_expert_layouts():
+    w = torch.zeros(4, 64, 40)
+    assert sg._expert_layout(w, "w") == (sg.ROW_MAJOR, 40, 2560)
+    assert sg._expert_layout(w.mT, "w") == (sg.COL_MAJOR, 40, 2560)
+    assert sg._expert_layout(torch.zeros(4, 64, 48)[..., :40], "w") == (sg.ROW_MAJOR, 48, 3072)
+    assert sg._expert_layout(w[::2], "w") == (sg.ROW_MAJOR, 40, 5120)
+    assert sg._expert_layout(torch.zeros(0, 8, 8), "w")[0] == sg.ROW_MAJOR
+    with pytest.raises(ValueError):
+        sg._expert_layout(torch.zeros(4, 8, 8, 2)[..., 0], "w")
+    with pytest.raises(ValueError):
+        sg._expert_layout(torch.zeros(8, 8), "w")
+
+
+def test_row_pitches():
+    assert sg._rows_ld(torch.zeros(5, 48)[:, :33], "x") == 48
+    assert sg._rows_ld(torch.zeros(1, 33), "x") == 48
+    for bad in (torch.zeros(8, 5).t(), torch.zeros(5, 16)[:, ::2], torch.zeros(1, 8).expand(5, 8), torch.zeros(5)):
+        with pytest.raises(ValueError):
+            sg._rows_ld(bad, "x")
