@@ -40,12 +40,14 @@ namespace {
 enum Knob {
   kKnobGrid, kKnobSched, kKnobSplitK, kKnobForceConfig, kKnobPair, kKnobForceLarge, kKnobGroupM, kKnobFp8Tn,
   kKnobLog, kKnobWaitLimitNs, kKnobEpiStore, kKnobGroupedSplit, kKnobPdl, kKnobGroupedTranspose, kKnobGroupedOrder,
+  kKnobRaggedRows,
   kNumKnobs
 };
 const char* const kKnobNames[kNumKnobs] = {
     "SMGEMM_GRID", "SMGEMM_SCHED", "SMGEMM_SPLITK", "SMGEMM_FORCE_CONFIG", "SMGEMM_PAIR", "SMGEMM_FORCE_LARGE",
     "SMGEMM_GROUP_M", "SMGEMM_FP8_TN", "SMGEMM_LOG", "SMGEMM_WAIT_LIMIT_NS", "SMGEMM_EPI_STORE",
-    "SMGEMM_SCHED_GROUPED_SPLIT", "SMGEMM_PDL", "SMGEMM_GROUPED_TRANSPOSE", "SMGEMM_GROUPED_ORDER"};
+    "SMGEMM_SCHED_GROUPED_SPLIT", "SMGEMM_PDL", "SMGEMM_GROUPED_TRANSPOSE", "SMGEMM_GROUPED_ORDER",
+    "SMGEMM_RAGGED_ROWS"};
 thread_local const char* g_knobs[kNumKnobs] = {};
 
 void refresh_knobs() {
@@ -359,13 +361,14 @@ struct MapKey3 {
 
 bool encode_3d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
                uint64_t depth, uint64_t row_stride_bytes, uint64_t depth_stride_bytes, uint32_t box_inner,
-               uint32_t box_outer) {
+               uint32_t box_outer, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   constexpr int kEntries = 16;
   thread_local MapKey3 keys[kEntries];
   thread_local CUtensorMap maps[kEntries];
   thread_local bool used[kEntries] = {};
   thread_local int next = 0;
-  const MapKey3 k{{base, inner, outer, row_stride_bytes, box_inner, box_outer, static_cast<int>(dt), 0}, depth,
+  const MapKey3 k{{base, inner, outer, row_stride_bytes, box_inner, box_outer, static_cast<int>(dt),
+                    static_cast<int>(swizzle)}, depth,
                   depth_stride_bytes};
   for (int i = 0; i < kEntries; ++i) {
     if (used[i] && keys[i].k == k.k && keys[i].depth == depth && keys[i].depth_stride == depth_stride_bytes) {
@@ -380,8 +383,7 @@ bool encode_3d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint6
   const cuuint32_t box[3] = {box_inner, box_outer, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   if (fn(map, dt, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+         swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return false;
   keys[next] = k;
   maps[next] = *map;
@@ -1055,20 +1057,28 @@ smgemm_status quantize_fp8_blockwise(const float* X, int64_t rows, int64_t cols,
 namespace {
 constexpr int64_t kInt8MaxK = 131071;  // 128 * 128 * K stays below 2^31
 
-// Token tiles of at most 64 rows when groups average at most 32 rows: the call then streams
-// the weights (memory bound), and the smaller row tiles leave shared memory for more stages
-// of weight loads in flight; above, 256 rows reuse each weight tile four times as often.
-bool ragged_narrow(int E, int64_t T) { return T <= 64 || T <= 32 * static_cast<int64_t>(E); }
-
+// Workspace of a ragged call: the ticket word, arrival counters of split tiles (two per
+// cluster), then `slots` partial tiles per cluster of 256 x `rows`. Counters first, so that
+// the partials start on a 256-byte boundary.
 size_t ragged_counter_bytes(int clusters) {
-  return (static_cast<size_t>(clusters) * 2 * sizeof(unsigned long long) + 255) / 256 * 256;
+  return (static_cast<size_t>(2 * clusters + 1) * sizeof(unsigned long long) + 255) / 256 * 256;
 }
-
-// Counters, then two partial tiles per cluster (a stream-K range cuts at most its first and
-// last tile) of 256 x TN; the weight gradient needs one of 256 x 256.
-size_t ragged_ws_bytes(int clusters, int tn, int slots_per_cluster) {
+size_t ragged_ws_bytes(int clusters, int rows, int slots) {
   return ragged_counter_bytes(clusters) +
-         static_cast<size_t>(clusters) * slots_per_cluster * 2 * 128 * static_cast<size_t>(tn) * sizeof(float);
+         static_cast<size_t>(clusters) * slots * 2 * 128 * static_cast<size_t>(rows) * sizeof(float);
+}
+// Rows of the widest tile a call with T rows can have.
+int ragged_tile_rows(int64_t T) { return static_cast<int>(std::min<int64_t>(256, (T + 31) / 32 * 32)); }
+
+extern "C++" {
+template <class Params>
+void ragged_workspace(Params& p, void* workspace, int clusters) {
+  p.ticket = static_cast<unsigned long long*>(workspace);
+  p.counters = p.ticket + 1;
+  p.slots = reinterpret_cast<float*>(static_cast<char*>(workspace) + ragged_counter_bytes(clusters));
+  p.gen = next_generation();
+  p.ticket_gen = static_cast<uint32_t>(p.gen) | 1u;
+}
 }
 
 smgemm_status check_groups(int E, int64_t T, int64_t N, int64_t K, const int32_t* offsets) {
@@ -1124,15 +1134,14 @@ smgemm_status ragged_impl(const RaggedArgs& a, void* workspace, size_t workspace
     if (i8 && ((reinterpret_cast<uintptr_t>(a.sa) & 3u) || (reinterpret_cast<uintptr_t>(a.sb) & 3u)))
       return SMGEMM_ERR_ALIGNMENT;
   }
-  const bool narrow = ragged_narrow(a.E, a.T);
-  const int tn = ragged_tile_tokens(narrow);
+  const int rows = ragged_tile_rows(a.T);
   const int64_t n_ft = (a.N + 255) / 256;
   if ((std::min<int64_t>(a.E, a.T) + a.T / 32) * n_ft > 0x7FFFFFFF) return SMGEMM_ERR_INVALID_ARG;  // tile numbers are 32-bit
   DevInfo d;
   if (current_device(d) != SMGEMM_OK) return SMGEMM_ERR_CUDA;
   const int P = ragged_max_clusters();
   if (P <= 0) return SMGEMM_ERR_CUDA;
-  if (workspace == nullptr || workspace_bytes < ragged_ws_bytes(P, tn, 2)) return SMGEMM_ERR_WORKSPACE;
+  if (workspace == nullptr || workspace_bytes < ragged_ws_bytes(P, rows, 2)) return SMGEMM_ERR_WORKSPACE;
   if (!aligned16(workspace)) return SMGEMM_ERR_ALIGNMENT;
 
   RaggedMaps m;
@@ -1149,6 +1158,18 @@ smgemm_status ragged_impl(const RaggedArgs& a, void* workspace, size_t workspace
                    : encode_3d(&m.w, dt, a.B, a.K, a.N, a.E, a.ldb * esz, depth_stride, bke, 128);
     for (int i = 0; i < 3; ++i) ok = ok && encode_2d(&m.x[i], dt, a.A, a.K, a.T, a.lda * esz, bke, 64 >> i);
     if (!ok) return SMGEMM_ERR_CUDA;
+  }
+  // Tile stores, as in gemm_bf16: only when a row of C is a whole number of 16-byte units.
+  const char* es = knob(kKnobEpiStore);
+  if ((a.N * elem_size(a.c_dtype)) % 16 == 0 && !(es != nullptr && std::strcmp(es, "direct") == 0)) {
+    const bool f32 = a.c_dtype == kF32;
+    const CUtensorMapDataType cdt = f32                      ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                    : a.c_dtype == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                           : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    if (!encode_2d(&m.c, cdt, a.C, a.N, a.T, a.ldc * elem_size(a.c_dtype), 32, f32 ? 16 : 32,
+                   f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+      return SMGEMM_ERR_CUDA;
+    p.tma_store = 1;
   }
   const uint32_t fmt = a.ab_dtype == kBF16 ? 1u : 0u;
   p.offsets = a.offsets;
@@ -1167,18 +1188,23 @@ smgemm_status ragged_impl(const RaggedArgs& a, void* workspace, size_t workspace
   p.ldc = a.ldc;
   p.sa = a.sa;
   p.sb = a.sb;
-  p.counters = static_cast<unsigned long long*>(workspace);
-  p.slots = reinterpret_cast<float*>(static_cast<char*>(workspace) + ragged_counter_bytes(P));
-  p.gen = next_generation();
+  ragged_workspace(p, workspace, P);
+  p.slot_words = 128 * rows;
+  const long long cap = env_ll(kKnobRaggedRows, 0);  // one of the kernel's tile heights, or 0
+  p.force_cap = cap == 256 || cap == 192 || cap == 128 || cap == 96 || cap == 64 || cap == 32 ? static_cast<int>(cap) : 0;
+  // One width fits all with T <= 32; with many tiles of the full height per cluster (were all
+  // rows one expert's) a lower height can only cost.
+  p.choose = a.T > 32 && (a.T / 256) * n_ft < 4 * static_cast<int64_t>(P) ? 1 : 0;
+  p.force_sched = sched_mode() == SchedMode::kDP ? 1 : (sched_mode() == SchedMode::kSK ? 2 : 0);
   p.wait_limit_cycles = wait_limit();
   // The tile count depends on the offsets: launch as many clusters as the most tiles and
   // K pieces there can be.
   const int64_t most = (std::min<int64_t>(a.E, a.T) + a.T / 32) * n_ft * std::max(1, p.kb_total / 4);
   const int clusters = static_cast<int>(std::min<int64_t>(most, P));
-  std::snprintf(config_text(), sizeof(g_last_config), "path=%s groups=%d rows=%d kb=%d grid=%d tile=256x%d", a.path,
-                a.E, p.T, p.kb_total, clusters, tn);
+  std::snprintf(config_text(), sizeof(g_last_config), "path=%s groups=%d rows=%d kb=%d grid=%d", a.path, a.E, p.T,
+                p.kb_total, clusters);
   if (env_ll(kKnobLog, 0)) std::fprintf(stderr, "[smgemm] %s\n", g_last_config);
-  return launch_status(launch_gemm_ragged(m, p, i8, narrow, clusters, stream));
+  return launch_status(launch_gemm_ragged(m, p, i8, clusters, stream));
 }
 }  // namespace
 
@@ -1188,7 +1214,7 @@ size_t smgemm_ragged_workspace_size(int E, int64_t T, int64_t N, int64_t K, int 
   DevInfo d;
   if (current_device(d) != SMGEMM_OK) return 0;
   if (kind == 2) return ragged_ws_bytes(wgrad_max_clusters(), 256, 1);
-  return ragged_ws_bytes(ragged_max_clusters(), ragged_tile_tokens(ragged_narrow(E, T)), 2);
+  return ragged_ws_bytes(ragged_max_clusters(), ragged_tile_rows(T), 2);
 }
 
 smgemm_status gemm_bf16_ragged(int E, int64_t T, int64_t N, int64_t K, const int32_t* offsets, const void* A,
@@ -1271,6 +1297,18 @@ smgemm_status gemm_bf16_ragged_wgrad(int E, int64_t T, int64_t N, int64_t K, con
     }
     const uint32_t fmt = bf16 ? 1u : 0u;
     WgradParams p{};
+    // Tile stores, as in gemm_bf16: only when a row of dB is a whole number of 16-byte units.
+    const char* es = knob(kKnobEpiStore);
+    if ((N * elem_size(c_dtype)) % 16 == 0 && !(es != nullptr && std::strcmp(es, "direct") == 0)) {
+      const uint64_t sz = static_cast<uint64_t>(elem_size(c_dtype));
+      const CUtensorMapDataType cdt = c_dtype == SMGEMM_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                      : c_dtype == SMGEMM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                               : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+      if (!encode_3d(&m.c, cdt, dB, N, K, E, ldc * sz, (E > 1 ? stride_c : K * ldc) * sz, c_dtype == SMGEMM_F32 ? 16 : 32,
+                     32, CU_TENSOR_MAP_SWIZZLE_64B))
+        return SMGEMM_ERR_CUDA;
+      p.tma_store = 1;
+    }
     p.offsets = offsets;
     p.E = E;
     p.T = static_cast<int>(T);
@@ -1283,13 +1321,12 @@ smgemm_status gemm_bf16_ragged_wgrad(int E, int64_t T, int64_t N, int64_t K, con
     p.c_dtype = c_dtype;
     p.ldc = ldc;
     p.stride_c = stride_c;
-    p.counters = static_cast<unsigned long long*>(workspace);
-    p.slots = reinterpret_cast<float*>(static_cast<char*>(workspace) + ragged_counter_bytes(P));
-    p.gen = next_generation();
+    ragged_workspace(p, workspace, P);
     p.wait_limit_cycles = wait_limit();
-    // Up to T / 512 pieces of one tile's rows run side by side.
-    const int64_t most = E * m_tiles * n_tiles * std::max<int64_t>(1, T / 512);
-    const int clusters = static_cast<int>(std::min<int64_t>(most, P));
+    // With fewer tiles than clusters, pieces of a tile's rows run side by side, as many for
+    // each tile; no more pieces than blocks of 512 rows.
+    const int64_t tiles = E * m_tiles * n_tiles;
+    const int clusters = static_cast<int>(tiles >= P ? P : tiles * std::min<int64_t>(P / tiles, std::max<int64_t>(1, T / 512)));
     std::snprintf(config_text(), sizeof(g_last_config), "path=ragged-wgrad groups=%d rows=%d tiles=%dx%d grid=%d", E,
                   p.T, p.m_tiles, p.n_tiles, clusters);
     if (env_ll(kKnobLog, 0)) std::fprintf(stderr, "[smgemm] %s\n", g_last_config);
@@ -1298,7 +1335,7 @@ smgemm_status gemm_bf16_ragged_wgrad(int E, int64_t T, int64_t N, int64_t K, con
   }
   if (dbias == nullptr) return SMGEMM_OK;
   return launch_status(
-      launch_ragged_dbias(D, bf16, ldd, static_cast<int>(T), static_cast<int>(N), offsets, E, dbias, stream));
+      launch_ragged_dbias(D, bf16, ldd, static_cast<int>(T), static_cast<int>(N), offsets, E, dbias, K > 0, stream));
 }
 
 smgemm_status quantize_int8_rowwise(const void* X, smgemm_dtype x_dtype, int64_t rows, int64_t cols, int64_t ldx,

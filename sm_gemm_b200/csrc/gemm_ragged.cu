@@ -16,12 +16,14 @@
 // the 3-D tensor map.
 //
 // Every CTA builds the group table (row bounds and first tiles) from the offsets in shared
-// memory, and from the tile count the schedule: whole waves of tiles round-robin over the
-// clusters, the ragged last wave cut along K (stream-K ranges, partials summed in K order
-// by the last contributor: deterministic, no CTA waits for another).
+// memory and, from estimates of the tiles' cost, picks the tile height and the schedule:
+// tiles drawn one by one (ragged_sched.cuh), or, when there are too few to go round, cut
+// along K (stream-K ranges, partials summed in K order by the last contributor: no CTA
+// waits for another). Which of a row's sums are split depends on the offsets alone, so
+// results are deterministic.
 //
-// Roles as in gemm_grouped.cu: warp 0 TMA producer, warp 1 MMA issuer (rank-0 CTA), warp 2
-// TMEM allocator, warp 3 group table, warps 4-11 epilogue.
+// Roles: warp 0 TMA producer (rank 0's also draws and publishes tiles), warp 1 MMA issuer
+// (rank-0 CTA), warp 2 TMEM allocator, warp 3 group table, warps 4-11 epilogue.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -29,6 +31,7 @@
 #include "ragged.h"
 #include "operands.cuh"
 #include "ragged.cuh"
+#include "ragged_sched.cuh"
 #include "sm100.cuh"
 
 namespace smg {
@@ -41,12 +44,77 @@ constexpr int kThreads = 32 * kEpiWarp0 + kEpiThreads;
 constexpr int kStageWarpBytes = 2048;  // epilogue transposition buffer per warp
 constexpr int kWBytes = 128 * 128;     // one CTA's weight tile of a stage: 128 features x 128 bytes of K
 
-// One tile: rows tok0 .. tok0 + ntok - 1 of expert e (MMA N = width), features from 256 ft.
-struct RItem {
-  int e, tok0, ntok, width, ft;
+// What the CTAs of a launch agree on, computed by each from the offsets.
+struct Plan {
+  int cap;          // rows of a tile at most
+  int tiles;        // of all groups and features
+  int width;        // widest tile of this call
+  int stream_k;     // static schedule with a split remainder instead of drawn tiles
 };
 
-__device__ __forceinline__ RItem locate(const RaggedParams& p, const int* bound, const int* tile0, int tn, int t) {
+// Tile heights to choose from: 256, 192, 128, 96, 64, 32 rows.
+constexpr int kNumCaps = 6;
+__device__ __forceinline__ int cap_of(int j) { return j < 2 ? 256 - 64 * j : 192 - 32 * j; }
+
+// Picks the tile height and the schedule, by one warp, from estimated cycles of the launch:
+// - one tile of w rows and kb K blocks: the MMA takes 2 w per block, the loads (128 x 128
+//   bytes of weights and 64 w bytes of rows per CTA, 64 bytes per cycle from L2) 256 + w,
+//   the longer for every w < 256; plus 700 for the tile's start and end;
+// - tiles drawn one by one: an even share plus on average half the longest tile for the
+//   last one; equal tiles need whole waves;
+// - cut along K: an even share plus the fix-up of a split tile (write, arrive, read back,
+//   epilogue: kFixup cycles, measured on narrow tiles);
+// - never faster than the active experts' weights come from HBM (9.6 cycles per 32 KB).
+// A lower cap has to be 2% better. With p.choose == 0 (T <= 32: one width; or so many tiles
+// that the highest is best) only the schedule is picked.
+constexpr float kFixup = 9000.0f;
+
+__device__ __forceinline__ Plan make_plan(const RaggedParams& p, const int* bound, int P, uint32_t lane) {
+  Plan pl{256, 0, 32, 0};
+  float best = 0.0f;
+  const float kb = static_cast<float>(p.kb_total), n_ft = static_cast<float>(p.n_ft);
+  const int first = p.force_cap != 0 ? (p.force_cap > 128 ? (256 - p.force_cap) / 64 : (192 - p.force_cap) / 32) : 0;
+  const int last = p.force_cap != 0 ? first : (p.choose ? kNumCaps - 1 : 0);
+#pragma unroll 1
+  for (int j = first; j <= last; ++j) {
+    const int cap = cap_of(j);
+    int tiles = 0, width = 32, active = 0;
+    unsigned rows = 0;  // summed 256 + w of the tiles, in units of 32
+#pragma unroll 1
+    for (int i = static_cast<int>(lane); i < p.E; i += 32) {
+      const int cnt = bound[i + 1] - bound[i];
+      if (cnt <= 0) continue;
+      const int w = tile_width(cnt, cap), nt = (cnt + w - 1) / w;
+      tiles += nt;
+      active += 1;
+      width = max(width, w);
+      rows += static_cast<unsigned>(nt) * static_cast<unsigned>(8 + (w >> 5));
+    }
+    tiles = __reduce_add_sync(0xffffffffu, tiles);
+    if (tiles == 0) break;  // no rows at all
+    active = __reduce_add_sync(0xffffffffu, active);
+    width = __reduce_max_sync(0xffffffffu, width);
+    rows = __reduce_add_sync(0xffffffffu, rows);
+    const float all = static_cast<float>(tiles) * n_ft;
+    const float sum = n_ft * (32.0f * kb * static_cast<float>(rows) + 700.0f * static_cast<float>(tiles));
+    const float longest = kb * static_cast<float>(256 + width) + 700.0f;
+    const float share = sum / static_cast<float>(P), hbm = static_cast<float>(active) * n_ft * kb * 9.6f;
+    float drawn = all <= static_cast<float>(P) ? longest
+                                               : fmaxf(share + 0.5f * longest, ceilf(all / static_cast<float>(P)) * (sum / all));
+    drawn = fmaxf(drawn, hbm);
+    const float split = fmaxf(share, hbm) + kFixup;
+    const int sk = p.force_sched == 2 || (p.force_sched == 0 && split < drawn);
+    const float t = sk ? split : drawn;
+    if (pl.tiles == 0 || t < 0.98f * best) {
+      best = t;
+      pl = Plan{cap, tiles * p.n_ft, width, sk};
+    }
+  }
+  return pl;
+}
+
+// The tile with number t (whole, no slot).
+__device__ __noinline__ RingItem resolve(const RaggedParams& p, const int* bound, const int* tile0, int cap, int t) {
   const int u = t / p.n_ft;
   int lo = 0, hi = p.E - 1;
   while (lo < hi) {
@@ -54,21 +122,28 @@ __device__ __forceinline__ RItem locate(const RaggedParams& p, const int* bound,
     if (tile0[mid] <= u) lo = mid;
     else hi = mid - 1;
   }
-  RItem it;
+  RingItem it;
   it.e = lo;
   const int r0 = bound[lo], r1 = bound[lo + 1];
-  const int w = tile_width(r1 - r0, tn);
-  TileSched ts{};
-  ts.m_tiles = tile0[lo + 1] - tile0[lo];
-  ts.n_tiles = p.n_ft;
-  ts.group_m = ts.m_tiles < 8 ? ts.m_tiles : 8;
-  int mt;
-  tile_coords(ts, t - tile0[lo] * p.n_ft, mt, it.ft);
-  it.tok0 = r0 + mt * w;
-  it.ntok = r1 - it.tok0 < w ? r1 - it.tok0 : w;
-  it.width = (it.ntok + 31) & ~31;
+  const int w = tile_width(r1 - r0, cap);
+  it.mt = 0;
+  it.nt = t - tile0[lo] * p.n_ft;
+  if (tile0[lo + 1] - tile0[lo] > 1) {
+    TileSched ts{};
+    ts.m_tiles = tile0[lo + 1] - tile0[lo];
+    ts.n_tiles = p.n_ft;
+    ts.group_m = ts.m_tiles < 8 ? ts.m_tiles : 8;
+    tile_coords(ts, it.nt, it.mt, it.nt);
+  }
+  it.row = r0 + it.mt * w;
+  it.nrow = r1 - it.row < w ? r1 - it.row : w;
+  it.kb0 = 0;
+  it.kb1 = p.kb_total;
+  it.tile = t;
   return it;
 }
+
+__device__ __forceinline__ int item_width(const RingItem& it) { return (it.nrow + 31) & ~31; }
 
 // The schedule of `tiles` tiles of kb K blocks over P clusters: whole waves data-parallel,
 // the R tiles of a ragged last wave as one stream-K range cut evenly over the clusters, at
@@ -99,18 +174,16 @@ __device__ __forceinline__ TileSched make_sched(int tiles, int kb, int P, int mi
 
 // 32 features (lanes) x 32 rows of C^T in registers -> C: scale, bias, activation, cast,
 // transposition through this warp's 2 KB buffer, 16-byte stores of whole row segments.
-// f0: the warp's first feature; row0: first row; nrow: rows to store (<= 32).
+// sb, b: the lane's column scale and bias; f0: the warp's first feature; row0: first row;
+// nrow: rows to store (<= 32).
 template <bool I8>
-__device__ __forceinline__ void emit_chunk(const RaggedParams& p, uint8_t* buf, int lane, int e, int f0, int row0,
-                                           int nrow, const uint32_t (&r)[32]) {
-  const int f = f0 + lane;
-  const bool live = f < p.N;
+__device__ __forceinline__ void emit_chunk(const RaggedParams& p, const CUtensorMap* tm_c, uint8_t* buf, int lane, float sb, float b, int f0,
+                                           int row0, int nrow, const uint32_t (&r)[32]) {
   float v[32];
   if (p.kb_total == 0) {  // no products: C = act(bias)
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] = 0.0f;
   } else if constexpr (I8) {
-    const float sb = live ? __ldg(p.sb + static_cast<long long>(e) * p.N + f) : 0.0f;
     const float sa = lane < nrow ? __ldg(p.sa + row0 + lane) : 0.0f;
     // int32 -> FP32 rounds sums of 2^24 and more to nearest (relative error 2^-24).
 #pragma unroll
@@ -120,10 +193,6 @@ __device__ __forceinline__ void emit_chunk(const RaggedParams& p, uint8_t* buf, 
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
   }
-  float b = 0.0f;
-  if (p.bias != nullptr && live) b = load_bias(static_cast<const char*>(p.bias) +
-                                               static_cast<long long>(e) * p.N * (p.bias_dtype == 0 ? 4 : 2),
-                                               p.bias_dtype, f);
   if (p.act != 0 && p.c_dtype == 0) {
     // FP32 output: activation in double, one copy of the code (see epi_bias_act32_f64).
 #pragma unroll 1
@@ -155,18 +224,36 @@ __device__ __forceinline__ void emit_chunk(const RaggedParams& p, uint8_t* buf, 
     }
   }
   const bool whole = f0 + 32 <= p.N;
+  // The buffer may still be read by this warp's last tile store.
+  if (lane == 0) bulk_wait_group_read<0>();
+  // Whole 32-row chunks leave as a TMA tile store (clipped to C's columns), so the warp does
+  // not wait for its stores; rows past the expert's end must stay as they are, so a last
+  // chunk is stored row by row.
+  const bool tma = p.tma_store && nrow == 32;
   if (p.c_dtype == 0) {
     float* C = static_cast<float*>(p.C);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {  // 16 rows of 128 bytes at a time
+      if (h == 1 && lane == 0) bulk_wait_group_read<0>();
       __syncwarp();
+      // 16-byte unit u of row j at u ^ (j & 7): the 128-byte swizzle of the store's map.
 #pragma unroll
-      for (int j = 0; j < 16; ++j) reinterpret_cast<float*>(buf)[j * 32 + lane] = v[16 * h + j];
+      for (int j = 0; j < 16; ++j)
+        reinterpret_cast<float*>(buf)[j * 32 + (((lane >> 2) ^ (j & 7)) << 2) + (lane & 3)] = v[16 * h + j];
+      if (tma) {
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(tm_c, smem_u32(buf), f0, row0 + 16 * h);
+          bulk_commit_group();
+        }
+        continue;
+      }
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int row = 4 * i + (lane >> 3), c = 4 * (lane & 7);
-        const float4 x = reinterpret_cast<const float4*>(buf)[row * 8 + (lane & 7)];
+        const float4 x = reinterpret_cast<const float4*>(buf)[row * 8 + ((lane & 7) ^ (row & 7))];
         if (16 * h + row < nrow) {
           float* dst = C + static_cast<long long>(row0 + 16 * h + row) * p.ldc + f0 + c;
           if (whole) {
@@ -182,7 +269,8 @@ __device__ __forceinline__ void emit_chunk(const RaggedParams& p, uint8_t* buf, 
     }
   } else {
     // Lane pairs exchange halves so that each 32-bit word holds two neighbouring features
-    // of one row: the even lane keeps row 2j, the odd lane row 2j + 1.
+    // of one row: the even lane keeps row 2j, the odd lane row 2j + 1. 16-byte unit u of row
+    // j sits at u ^ ((j >> 1) & 3): the 64-byte swizzle of the store's map.
     const bool odd = lane & 1;
     __syncwarp();
 #pragma unroll
@@ -198,14 +286,23 @@ __device__ __forceinline__ void emit_chunk(const RaggedParams& p, uint8_t* buf, 
         const __half2 t = __floats2half2_rn(lo, hi);
         w = *reinterpret_cast<const uint32_t*>(&t);
       }
-      reinterpret_cast<uint32_t*>(buf)[(2 * j + (odd ? 1 : 0)) * 16 + (lane >> 1)] = w;
+      reinterpret_cast<uint32_t*>(buf)[(2 * j + (odd ? 1 : 0)) * 16 + (((lane >> 3) ^ (j & 3)) << 2) + ((lane >> 1) & 3)] = w;
+    }
+    if (tma) {
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_2d(tm_c, smem_u32(buf), f0, row0);
+        bulk_commit_group();
+      }
+      return;
     }
     __syncwarp();
     uint16_t* C = static_cast<uint16_t*>(p.C);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int row = 8 * i + (lane >> 2), c = 8 * (lane & 3);
-      const uint4 x = reinterpret_cast<const uint4*>(buf)[row * 4 + (lane & 3)];
+      const uint4 x = reinterpret_cast<const uint4*>(buf)[row * 4 + ((lane & 3) ^ ((row >> 1) & 3))];
       if (row < nrow) {
         uint16_t* dst = C + static_cast<long long>(row0 + row) * p.ldc + f0 + c;
         if (whole) {
@@ -222,13 +319,18 @@ __device__ __forceinline__ void emit_chunk(const RaggedParams& p, uint8_t* buf, 
 }
 
 // Partial sums of a split tile: FP32 partials add as floats, int32 partials as integers.
-template <bool I8>
-__device__ __forceinline__ void slot_add32(const float* slot, int r_local, int col0, uint32_t (&v)[32]) {
+// Two contributors' loads are in flight before the first add.
+__device__ __forceinline__ void slot_load32(const float* slot, int r_local, int col0, uint4 (&t)[8]) {
   const uint4* s4 = reinterpret_cast<const uint4*>(slot);
 #pragma unroll
+  for (int q = 0; q < 8; ++q) t[q] = __ldcg(s4 + ((col0 >> 2) + q) * 128 + r_local);
+}
+
+template <bool I8>
+__device__ __forceinline__ void slot_add32(const uint4 (&t)[8], uint32_t (&v)[32]) {
+#pragma unroll
   for (int q = 0; q < 8; ++q) {
-    const uint4 t = __ldcg(s4 + ((col0 >> 2) + q) * 128 + r_local);
-    const uint32_t x[4] = {t.x, t.y, t.z, t.w};
+    const uint32_t x[4] = {t[q].x, t[q].y, t[q].z, t[q].w};
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
       if constexpr (I8) v[4 * q + h] += x[h];
@@ -238,39 +340,47 @@ __device__ __forceinline__ void slot_add32(const float* slot, int r_local, int c
 }
 }  // namespace
 
-template <bool I8, int TN, int STAGES>
+namespace {
+constexpr int kMaxStages = 12;
+constexpr int kStageSpace = 6 * (kWBytes + 128 * 128);  // six stages of the widest tiles
+constexpr int kBars = 2 * kMaxStages + 6 + 2 * kRing;
+}  // namespace
+
+template <bool I8>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_ragged_kernel(const __grid_constant__ RaggedMaps maps, const __grid_constant__ RaggedParams p) {
-  constexpr int X_BYTES = (TN / 2) * 128;
-  constexpr int STAGE_BYTES = kWBytes + X_BYTES;
   constexpr int BKE = I8 ? 128 : 64;  // elements of K per block of 128 bytes
-  constexpr int SLOT = 128 * TN;
-  constexpr int TCOLS = 2 * TN;       // two accumulators
+  constexpr int TN = 256;             // columns of an accumulator
   constexpr int kMinKb = 4;           // fewest K blocks of a stream-K piece
 
   extern __shared__ uint8_t smem_raw[];
   const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* smem_gen = smem_raw + (smem_base - smem_u32(smem_raw));
-  uint8_t* staging = smem_gen + STAGES * STAGE_BYTES;
-  const uint32_t bar_base = smem_base + STAGES * STAGE_BYTES + kEpiWarps * kStageWarpBytes;
+  uint8_t* staging = smem_gen + kStageSpace;
+  const uint32_t ring_base = smem_base + kStageSpace + kEpiWarps * kStageWarpBytes;
+  const uint32_t bar_base = ring_base + kRing * kRingEntryBytes;
   auto full_bar = [&](int s) { return bar_base + 8u * s; };
-  auto empty_bar = [&](int s) { return bar_base + 8u * (STAGES + s); };
-  auto tfull_bar = [&](int b) { return bar_base + 8u * (2 * STAGES + b); };
-  auto tempty_bar = [&](int b) { return bar_base + 8u * (2 * STAGES + 2 + b); };
-  const uint32_t drain_bar = bar_base + 8u * (2 * STAGES + 4);
-  uint8_t* misc = smem_gen + STAGES * STAGE_BYTES + kEpiWarps * kStageWarpBytes + 8 * (2 * STAGES + 5);
+  auto empty_bar = [&](int s) { return bar_base + 8u * (kMaxStages + s); };
+  auto tfull_bar = [&](int b) { return bar_base + 8u * (2 * kMaxStages + b); };
+  auto tempty_bar = [&](int b) { return bar_base + 8u * (2 * kMaxStages + 2 + b); };
+  const uint32_t drain_bar = bar_base + 8u * (2 * kMaxStages + 4);
+  const uint32_t epi_bar = bar_base + 8u * (2 * kMaxStages + 5);
+  const uint32_t rfull_bar = epi_bar + 8u, rempty_bar = rfull_bar + 8u * kRing;
+  uint8_t* misc = smem_gen + kStageSpace + kEpiWarps * kStageWarpBytes + kRing * kRingEntryBytes + 8 * kBars;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 4);
   volatile int* reduce_flag = reinterpret_cast<volatile int*>(misc + 8);
-  int* bound = reinterpret_cast<int*>(misc + 16);  // [E + 1]
+  Plan* plan_sh = reinterpret_cast<Plan*>(misc + 16);
+  int* bound = reinterpret_cast<int*>(misc + 32);  // [E + 1]
   int* tile0 = bound + p.E + 1;                    // [E + 1]
 
   const uint32_t warp = warp_id(), lane = lane_id();
   const uint32_t rank = cluster_ctarank();
   const int cluster = blockIdx.x >> 1;
+  const int P = static_cast<int>(gridDim.x >> 1);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
+    for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
     }
@@ -279,6 +389,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(tempty_bar(b), 2 * kEpiWarps);
     }
     mbar_init(drain_bar, 1);
+    mbar_init(epi_bar, kEpiWarps);
+    for (int s = 0; s < kRing; ++s) {
+      mbar_init(rfull_bar + 8 * s, 1);
+      mbar_init(rempty_bar + 8 * s, ring_readers(kEpiWarps));
+    }
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -286,21 +401,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&maps.w);
 #pragma unroll
     for (int i = 0; i < 3; ++i) tma_prefetch_desc(&maps.x[i]);
+    tma_prefetch_desc(&maps.c);
   }
   if (warp == 2) {
-    tmem_alloc_pair(smem_u32(const_cast<uint32_t*>(tmem_slot)), TCOLS);
+    tmem_alloc_pair(smem_u32(const_cast<uint32_t*>(tmem_slot)), 2 * TN);
     tmem_relinquish_pair();
   }
   pdl_launch_dependents();
   pdl_wait();
-  if (warp == 3) build_group_table(p.offsets, p.E, p.T, TN, lane, bound, tile0);
+  if (warp == 3) {
+    group_bounds(p.offsets, p.E, p.T, lane, bound);
+    __syncwarp();
+    const Plan pl = make_plan(p, bound, P, lane);
+    group_tiles(bound, p.E, pl.cap, lane, tile0);
+    if (lane == 0) *plan_sh = pl;
+  }
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // both CTAs' barriers exist before any remote arrive or copy targets them
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const TileSched s = make_sched(tile0[p.E] * p.n_ft, p.kb_total, static_cast<int>(gridDim.x >> 1), kMinKb);
+  const Plan plan = *plan_sh;
   const uint64_t limit = p.wait_limit_cycles;
+  const bool drawn = plan.stream_k == 0 && plan.tiles > P;
+  const int stage_bytes = kWBytes + plan.width * 64;
+  const int stages = min(kMaxStages, kStageSpace / stage_bytes);
+  const int slot_words = p.slot_words;
+  Ring ring{ring_base, rfull_bar, rempty_bar, 0};
 
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
@@ -308,19 +435,67 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 0;
     long long issued = 0;
     bool ok = true;
-    WorkIter wi;
-    wi.init(s, cluster);
+    // The cluster's first tile is known without a draw: both CTAs' producers start on it at
+    // once. Its entry for the other warps is published once its first copies are issued.
+    TileSched s{};
+    WorkIter wi{};
     Seg seg;
-    while (ok && wi.next(s, seg)) {
-      const RItem it = locate(p, bound, tile0, TN, seg.tile);
-      const int rows = it.width >> 1;  // this CTA's half of the tile's rows: a multiple of 16
-      const int w_row = it.ft * 256 + static_cast<int>(rank) * 128;
-      const int x_row = it.tok0 + static_cast<int>(rank) * rows;
+    RingItem it{-1, 0, 0, 0, 0, 0, 0, 0};
+    // The next item of the static schedule with a split remainder.
+    auto static_next = [&]() {
+      RingItem x{-1, 0, 0, 0, 0, 0, 0, 0};
+      if (wi.next(s, seg)) {
+        x = resolve(p, bound, tile0, plan.cap, seg.tile);
+        x.kb0 = seg.kb0;
+        x.kb1 = seg.kb1;
+        x.tile |= seg.slot << 31;
+      }
+      return x;
+    };
+    if (plan.stream_k) {
+      s = make_sched(plan.tiles, p.kb_total, P, kMinKb);
+      wi.init(s, cluster);
+      it = static_next();
+    } else if (cluster < plan.tiles) {
+      it = resolve(p, bound, tile0, plan.cap, cluster);
+    }
+    if (it.e < 0) {
+      if (rank == 0) ring.publish(it, abort_flag, limit);
+      else ring.take(it, abort_flag, limit);
+      ok = false;
+    }
+    bool first = true;
+    while (ok) {
+      unsigned ticket = 0;
+      if (rank == 0 && drawn && lane == 0) ticket = draw_ticket(p.ticket, p.ticket_gen, P, plan.tiles);
+      RingItem next{-1, 0, 0, 0, 0, 0, 0, 0};
+      // The next tile is resolved and published (rank 0) in the middle of this one, once the
+      // stages are full and the loads wait for the MMA anyway: done between two tiles it left
+      // the memory queue to drain (82 -> 91 us on 64 rows over 27 experts of 2048 x 4096).
+      auto handover = [&]() {
+        if (first) {  // this tile's own entry; rank 1 knows the tile and only moves the ring on
+          RingItem same = it;
+          if (!(rank == 0 ? ring.publish(it, abort_flag, limit) : ring.take(same, abort_flag, limit))) return false;
+          first = false;
+        }
+        if (rank != 0) return true;
+        if (plan.stream_k) {
+          next = static_next();
+        } else if (drawn) {
+          ticket = __shfl_sync(0xffffffffu, ticket, 0);
+          if (ticket < static_cast<unsigned>(plan.tiles)) next = resolve(p, bound, tile0, plan.cap, static_cast<int>(ticket));
+        }
+        return ring.publish(next, abort_flag, limit);
+      };
+      const int k_next = min(it.kb1 - 1, it.kb0 + stages - 1);
+      const int rows = item_width(it) >> 1;  // this CTA's half of the tile's rows: a multiple of 16
+      const int w_row = it.nt * 256 + static_cast<int>(rank) * 128;
+      const int x_row = it.row + static_cast<int>(rank) * rows;
       const uint32_t tx_bytes = 2u * (kWBytes + rows * 128);
-      for (int kb = seg.kb0; kb < seg.kb1; ++kb) {
+      for (int kb = it.kb0; kb < it.kb1; ++kb) {
         const bool w = mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, limit);
         if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
-        const uint32_t sw = smem_base + stage * STAGE_BYTES;
+        const uint32_t sw = smem_base + stage * stage_bytes;
         const uint32_t sx = sw + kWBytes;
         const uint32_t leader_full = mapa_shared(full_bar(stage), 0);
         if (elect_one()) {
@@ -343,16 +518,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         ++issued;
-        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        if (++stage == stages) { stage = 0; phase ^= 1u; }
+        if (kb == k_next && !handover()) { ok = false; break; }
+      }
+      if (ok && it.kb0 == it.kb1) ok = handover();  // K == 0
+      if (!ok) break;
+      if (rank == 0) {
+        it = next;
+        ok = it.e >= 0;
+      } else {
+        ok = ring.take(it, abort_flag, limit);
       }
     }
-    if (!ok && rank == 0 && lane == 0) {
+    if (*abort_flag != 0 && rank == 0 && lane == 0) {
       // Wait (bounded, independent of the abort flag) for copies still in flight.
       int st = stage;
       uint32_t ph = phase;
       volatile int no_abort = 0;
-      for (long long i = 0; i < issued && i < STAGES; ++i) {
-        if (--st < 0) { st = STAGES - 1; ph ^= 1u; }
+      for (long long i = 0; i < issued && i < stages; ++i) {
+        if (--st < 0) { st = stages - 1; ph ^= 1u; }
         mbar_wait(full_bar(st), ph, &no_abort, limit);
       }
     }
@@ -362,26 +546,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 0;
     int local = 0;
     bool ok = true;
-    WorkIter wi;
-    wi.init(s, cluster);
-    Seg seg;
-    while (ok && wi.next(s, seg)) {
-      const RItem it = locate(p, bound, tile0, TN, seg.tile);
-      const uint32_t idesc = p.idesc | (static_cast<uint32_t>(it.width >> 3) << 17);
+    RingItem it;
+    ok = ring.take(it, abort_flag, limit);
+    while (ok) {
+      const uint32_t idesc = p.idesc | (static_cast<uint32_t>(item_width(it) >> 3) << 17);
       const int acc = local & 1;
       const uint32_t acc_phase = (local >> 1) & 1;
       if (!__all_sync(0xffffffffu, mbar_wait(tempty_bar(acc), acc_phase ^ 1u, abort_flag, limit))) break;
       tc_fence_after();
       const uint32_t d_tmem = tmem_base + acc * TN;
-      for (int kb = seg.kb0; kb < seg.kb1; ++kb) {
+      bool more = true;
+      const int kb0 = it.kb0, kb1 = it.kb1;
+      if (kb0 == kb1) more = ring.take(it, abort_flag, limit);
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (kb == kb1 - 1) more = ring.take(it, abort_flag, limit);  // behind the MMAs in flight
         if (!__all_sync(0xffffffffu, mbar_wait(full_bar(stage), phase, abort_flag, limit))) { ok = false; break; }
         tc_fence_after();
-        const uint32_t sw = smem_base + stage * STAGE_BYTES;
+        const uint32_t sw = smem_base + stage * stage_bytes;
         const uint32_t sx = sw + kWBytes;
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint32_t accum = (kb > seg.kb0 || k > 0) ? 1u : 0u;
+            const uint32_t accum = (kb > kb0 || k > 0) ? 1u : 0u;
             const uint64_t xd = sdesc_sw128(sx + 32 * k, 16, 1024);
             if constexpr (I8) umma_i8_pair(d_tmem, sdesc_sw128(sw + 32 * k, 16, 1024), xd, idesc, accum);
             else umma_f16_pair(d_tmem, operand_desc<128, 64>(sw, p.w_mn_major, k), xd, idesc, accum);
@@ -389,12 +575,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma_commit_pair(empty_bar(stage), 0x3);
         }
         __syncwarp();
-        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        if (++stage == stages) { stage = 0; phase ^= 1u; }
       }
       if (!ok) break;
       if (elect_one()) umma_commit_pair(tfull_bar(acc), 0x3);
       __syncwarp();
       ++local;
+      ok = more;
     }
     if (elect_one()) umma_commit_pair(drain_bar, 0x1);
     __syncwarp();
@@ -408,99 +595,103 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_addr = static_cast<uint32_t>(q * 32) << 16;
     const int epi_tid = threadIdx.x - kEpiWarp0 * 32;
     uint8_t* buf = staging + (warp - kEpiWarp0) * kStageWarpBytes;
+    EpiBarrier epi{epi_bar, 0};
+    TileSched s{};
+    if (plan.stream_k) s = make_sched(plan.tiles, p.kb_total, P, kMinKb);
     int local = 0;
-    bool dead = false;
-    WorkIter wi;
-    wi.init(s, cluster);
-    Seg seg;
-    while (wi.next(s, seg)) {
-      const RItem it = locate(p, bound, tile0, TN, seg.tile);
+    RingItem it;
+    while (ring.take(it, abort_flag, limit)) {
       const int acc = local & 1;
       const uint32_t acc_phase = (local >> 1) & 1;
-      if (!dead) dead = !mbar_wait(tfull_bar(acc), acc_phase, abort_flag, limit);
-      dead = __any_sync(0xffffffffu, dead);
-      const int f0 = it.ft * 256 + static_cast<int>(rank) * 128 + q * 32;
-      const int chunks = it.width >> 5;
-      const uint32_t tacc = tmem_base + lane_addr + acc * TN;
-      const bool whole = seg.kb0 == 0 && seg.kb1 == s.kb_total;
-      auto emit = [&](int c, const uint32_t(&r)[32]) {
-        const int n = it.ntok - 32 * c;
-        if (f0 < p.N) emit_chunk<I8>(p, buf, static_cast<int>(lane), it.e, f0, it.tok0 + 32 * c, n < 32 ? n : 32, r);
-      };
-      float* my_slot = p.slots + ((static_cast<size_t>(cluster) * 2 + seg.slot) * 2 + rank) * SLOT;
-      if (!dead) {
-        tc_fence_after();
-#pragma unroll 1
-        for (int c = half; c < chunks; c += 2) {
-          uint32_t r[32];
-          tmem_ld_32x32b_x32_sync(tacc + c * 32, r);
-          if (whole) {
-            emit(c, r);
-          } else {
-            float v[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-            slot_store<32>(my_slot, r_local, c * 32, v);
-          }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
+      const int f0 = it.nt * 256 + static_cast<int>(rank) * 128 + q * 32;
+      // The lane's column scale and bias, loaded while the tile's MMAs run.
+      const bool live = f0 + static_cast<int>(lane) < p.N;
+      const long long col = static_cast<long long>(it.e) * p.N + f0 + lane;
+      float sb = 0.0f, b = 0.0f;
+      if (I8 && live && p.kb_total > 0) sb = __ldg(p.sb + col);
+      if (p.bias != nullptr && live) {
+        if (p.bias_dtype == 0) b = __ldg(static_cast<const float*>(p.bias) + col);
+        else if (p.bias_dtype == 1) b = __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[col]);
+        else b = __half2float(static_cast<const __half*>(p.bias)[col]);
       }
+      if (!__all_sync(0xffffffffu, mbar_wait(tfull_bar(acc), acc_phase, abort_flag, limit))) break;
+      const int chunks = item_width(it) >> 5;
+      const uint32_t tacc = tmem_base + lane_addr + acc * TN;
+      const bool whole = it.kb0 == 0 && it.kb1 == p.kb_total;
+      auto emit = [&](int c, const uint32_t(&r)[32]) {
+        const int n = it.nrow - 32 * c;
+        if (f0 < p.N) emit_chunk<I8>(p, &maps.c, buf, static_cast<int>(lane), sb, b, f0, it.row + 32 * c, n < 32 ? n : 32, r);
+      };
+      float* my_slot = p.slots + ((static_cast<size_t>(cluster) * 2 + ring_slot(it)) * 2 + rank) * slot_words;
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = half; c < chunks; c += 2) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32_sync(tacc + c * 32, r);
+        if (whole) {
+          emit(c, r);
+        } else {
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+          slot_store<32>(my_slot, r_local, c * 32, v);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(tempty_bar(acc), 0));
       if (!whole) {
         // The last contributor to the tile (per rank) sums the partials in K order.
-        const long long t_sk = seg.tile - s.dp_tiles;
+        const long long t_sk = ring_tile(it) - s.dp_tiles;
         const int c_lo = sk_owner(s, t_sk * s.kb_total);
         const int c_hi = sk_owner(s, (t_sk + 1) * s.kb_total - 1);
         __threadfence();
-        named_barrier_sync(1, kEpiThreads);
+        if (!epi.sync(abort_flag, limit)) break;
         if (epi_tid == 0) {
-          const bool any_dead = *abort_flag != 0;
           const int n = c_hi - c_lo + 1;  // every cluster's range is non-empty
-          const int old = any_dead ? -1 : counter_arrive(p.counters + t_sk * 2 + rank, p.gen, n);
-          *reduce_flag = (!any_dead && old == n - 1);
+          *reduce_flag = counter_arrive(p.counters + t_sk * 2 + rank, p.gen, n) == n - 1;
         }
-        named_barrier_sync(1, kEpiThreads);
+        if (!epi.sync(abort_flag, limit)) break;
         if (*reduce_flag) {
           __threadfence();
+          auto slot_of = [&](int cc) {
+            return p.slots + ((static_cast<size_t>(cc) * 2 + sk_slot_of(s, cc, t_sk)) * 2 + rank) * slot_words;
+          };
 #pragma unroll 1
           for (int c = half; c < chunks; c += 2) {
             uint32_t v[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = 0u;
 #pragma unroll 1
-            for (int cc = c_lo; cc <= c_hi; ++cc) {
-              const float* src = p.slots + ((static_cast<size_t>(cc) * 2 + sk_slot_of(s, cc, t_sk)) * 2 + rank) * SLOT;
-              slot_add32<I8>(src, r_local, c * 32, v);
+            for (int cc = c_lo; cc <= c_hi; cc += 2) {
+              uint4 t0[8], t1[8];
+              slot_load32(slot_of(cc), r_local, c * 32, t0);
+              if (cc < c_hi) slot_load32(slot_of(cc + 1), r_local, c * 32, t1);
+              slot_add32<I8>(t0, v);
+              if (cc < c_hi) slot_add32<I8>(t1, v);
             }
             emit(c, v);
           }
         }
-        named_barrier_sync(1, kEpiThreads);
+        if (!epi.sync(abort_flag, limit)) break;  // reduce_flag has been read
       }
       ++local;
     }
+    if (lane == 0) bulk_wait_group<0>();  // this warp's tile stores have landed
   }
 
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // the peer stays resident until the rank-0 MMA issuer has drained
   tc_fence_after();
-  if (warp == 2) tmem_dealloc_pair(tmem_base, TCOLS);
+  if (warp == 2) tmem_dealloc_pair(tmem_base, 2 * TN);
 }
 
 namespace {
-constexpr int kWideStages = 6, kNarrowStages = 9;
+constexpr int kSmem = 1024 + kStageSpace + kEpiWarps * kStageWarpBytes + kRing * kRingEntryBytes + 8 * kBars + 32 +
+                      2 * (kRaggedMaxGroups + 1) * static_cast<int>(sizeof(int));
+static_assert(kSmem <= 232448, "shared memory budget");
 
-template <int TN, int STAGES>
-constexpr int smem_bytes(int E) {
-  return 1024 + STAGES * (kWBytes + (TN / 2) * 128) + kEpiWarps * kStageWarpBytes + 8 * (2 * STAGES + 5) + 16 +
-         2 * (E + 1) * static_cast<int>(sizeof(int));
-}
-static_assert(smem_bytes<256, kWideStages>(kRaggedMaxGroups) <= 232448, "shared memory budget");
-static_assert(smem_bytes<64, kNarrowStages>(kRaggedMaxGroups) <= 232448, "shared memory budget");
-
-template <bool I8, int TN, int STAGES>
 cudaLaunchConfig_t config(int clusters, cudaStream_t stream, cudaLaunchAttribute* attr) {
   cudaLaunchConfig_t cfg = {};
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -509,34 +700,34 @@ cudaLaunchConfig_t config(int clusters, cudaStream_t stream, cudaLaunchAttribute
   attr[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3(2 * clusters, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem_bytes<TN, STAGES>(kRaggedMaxGroups);
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cfg;
 }
 
-template <bool I8, int TN, int STAGES>
+template <bool I8>
 int max_clusters_of() {
-  if (smem_opt_in<gemm_ragged_kernel<I8, TN, STAGES>>(smem_bytes<TN, STAGES>(kRaggedMaxGroups)) != cudaSuccess) return 0;
+  if (smem_opt_in<gemm_ragged_kernel<I8>>(kSmem) != cudaSuccess) return 0;
   cudaLaunchAttribute attr[1];
-  cudaLaunchConfig_t cfg = config<I8, TN, STAGES>(1, nullptr, attr);
+  cudaLaunchConfig_t cfg = config(1, nullptr, attr);
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, gemm_ragged_kernel<I8, TN, STAGES>, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, gemm_ragged_kernel<I8>, &cfg) != cudaSuccess) {
     cudaGetLastError();
     n = 0;
   }
   return n;
 }
 
-template <bool I8, int TN, int STAGES>
+template <bool I8>
 cudaError_t launch_of(const RaggedMaps& m, const RaggedParams& p, int clusters, cudaStream_t stream) {
-  cudaError_t e = smem_opt_in<gemm_ragged_kernel<I8, TN, STAGES>>(smem_bytes<TN, STAGES>(kRaggedMaxGroups));
+  cudaError_t e = smem_opt_in<gemm_ragged_kernel<I8>>(kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
-  cudaLaunchConfig_t cfg = config<I8, TN, STAGES>(clusters, stream, attr);
+  cudaLaunchConfig_t cfg = config(clusters, stream, attr);
   add_pdl_attr(cfg, attr);
-  e = cudaLaunchKernelEx(&cfg, gemm_ragged_kernel<I8, TN, STAGES>, m, p);
+  e = cudaLaunchKernelEx(&cfg, gemm_ragged_kernel<I8>, m, p);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
@@ -546,21 +737,14 @@ int ragged_max_clusters() {
   static std::atomic<int> cached{-1};
   int n = cached.load();
   if (n >= 0) return n;
-  const int c[4] = {max_clusters_of<false, 256, kWideStages>(), max_clusters_of<false, 64, kNarrowStages>(),
-                    max_clusters_of<true, 256, kWideStages>(), max_clusters_of<true, 64, kNarrowStages>()};
-  n = c[0];
-  for (int i = 1; i < 4; ++i) n = c[i] < n ? c[i] : n;
+  const int a = max_clusters_of<false>(), b = max_clusters_of<true>();
+  n = a < b ? a : b;
   cached.store(n);
   return n;
 }
 
-cudaError_t launch_gemm_ragged(const RaggedMaps& m, const RaggedParams& p, bool i8, bool narrow, int clusters,
-                               cudaStream_t stream) {
-  if (i8)
-    return narrow ? launch_of<true, 64, kNarrowStages>(m, p, clusters, stream)
-                  : launch_of<true, 256, kWideStages>(m, p, clusters, stream);
-  return narrow ? launch_of<false, 64, kNarrowStages>(m, p, clusters, stream)
-                : launch_of<false, 256, kWideStages>(m, p, clusters, stream);
+cudaError_t launch_gemm_ragged(const RaggedMaps& m, const RaggedParams& p, bool i8, int clusters, cudaStream_t stream) {
+  return i8 ? launch_of<true>(m, p, clusters, stream) : launch_of<false>(m, p, clusters, stream);
 }
 
 unsigned take_error_word_ragged() { return take_error_word(); }

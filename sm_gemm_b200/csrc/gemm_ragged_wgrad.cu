@@ -11,9 +11,11 @@
 // expert's rows from where they are and the rest from rows past T, which TMA fills with
 // zeros. The extra copies are issued once per tile.
 //
-// Tiles go round-robin over the clusters; the tiles of a ragged last wave are split along
-// the rows into S pieces, summed in row order by the last to finish (deterministic).
-// Roles as in gemm_grouped.cu.
+// A tile costs its expert's rows, so tiles are drawn one by one (ragged_sched.cuh), the
+// experts with the most rows first; with fewer tiles than clusters each is split along its
+// rows into pieces, summed in row order by the last to finish (deterministic).
+// Roles as in gemm_ragged.cu. dbias runs beside the product: its kernel is launched
+// programmatically, reads D while the product's CTAs run, and ends after them.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -21,6 +23,7 @@
 #include "operands.cuh"
 #include "ragged.cuh"
 #include "ragged.h"
+#include "ragged_sched.cuh"
 #include "sm100.cuh"
 
 namespace smg {
@@ -33,81 +36,184 @@ constexpr int kThreads = 32 * kEpiWarp0 + kEpiThreads;
 constexpr int kEpiCols = 128;  // tile columns per epilogue warp
 constexpr int kTileN = 256;
 constexpr int kTcols = 512;
-constexpr int kBK = 64, kStages = 6;
+constexpr int kBK = 64, kStages = 5;
 constexpr int kOpBytes = 128 * kBK * 2;  // one CTA's operand tile of a stage
 constexpr int kStageBytes = 2 * kOpBytes;
 
-// One piece of a tile: rows kb0*64 .. of expert e; unit >= 0 marks a piece of a split tile.
-struct WItem {
-  int tile, e, mt, nt, row0, cnt, kb0, kb1, unit;
-};
+constexpr int kStageBufs = 2;          // epilogue staging buffers per warp
+constexpr int kStageWarpBytes = kStageBufs * 2048;
+constexpr int kBars = 2 * kStages + 6 + 2 * kRing;
+constexpr int kSortGroups = 256;       // experts ordered by their rows (a quadratic ranking)
+constexpr int kMinKb = 8;              // fewest row blocks of a split tile's piece
 
 struct WSched {
-  int tiles, split_tiles, splits, per_group, P;
+  int tiles, per_group, P, splits;  // splits: most pieces of a tile (1: whole tiles)
 };
 
-struct WIter {
-  int next_dp, cluster;
-  bool unit_pending;
+// Tile t, whole.
+__device__ __forceinline__ RingItem resolve(const WgradParams& p, const WSched& s, const int* bound, const int* order,
+                                            int t) {
+  RingItem it;
+  const int g = t / s.per_group;
+  it.e = order[g];
+  TileSched ts{};
+  ts.m_tiles = p.m_tiles;
+  ts.n_tiles = p.n_tiles;
+  ts.group_m = p.m_tiles < 8 ? p.m_tiles : 8;
+  tile_coords(ts, t - g * s.per_group, it.mt, it.nt);
+  it.row = bound[it.e];
+  it.nrow = bound[it.e + 1] - it.row;
+  it.kb0 = 0;
+  it.kb1 = (it.nrow + kBK - 1) / kBK;
+  it.tile = t;
+  return it;
+}
 
-  __device__ __forceinline__ void init(const WSched& s, int c) {
-    cluster = c;
-    next_dp = c;
-    unit_pending = c < s.split_tiles * s.splits;
+// Pieces of a tile with kb row blocks.
+__device__ __forceinline__ int pieces_of(const WSched& s, int kb) { return max(1, min(s.splits, kb / kMinKb)); }
+
+// 32 rows (lanes) x 32 columns of a gradient -> dB as TMA tile stores of 64 bytes x 32 rows
+// (two for FP32), staged in alternating 2 KB buffers: the warp goes on while they are
+// written. With 16-byte stores from registers the epilogue bounded small experts' tiles
+// (64 experts of 193 rows, 2048 x 1000 FP32 gradients: 161 us). 16-byte unit j of row r sits
+// at j ^ ((r >> 1) & 3), the map's 64-byte swizzle.
+__device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t buf, int lane, int col, int row0, int e,
+                                          const uint32_t* w) {
+  if (lane == 0) bulk_wait_group_read<kStageBufs - 1>();
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 64 + 16 * (j ^ ((lane >> 1) & 3))),
+                 "r"(w[4 * j]), "r"(w[4 * j + 1]), "r"(w[4 * j + 2]), "r"(w[4 * j + 3])
+                 : "memory");
+  fence_proxy_async_shared();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_3d(map, buf, col, row0, e);
+    bulk_commit_group();
   }
-  __device__ __forceinline__ void fill(const WgradParams& p, const WSched& s, const int* bound, WItem& it) {
-    it.e = it.tile / s.per_group;
-    TileSched ts{};
-    ts.m_tiles = p.m_tiles;
-    ts.n_tiles = p.n_tiles;
-    ts.group_m = p.m_tiles < 8 ? p.m_tiles : 8;
-    tile_coords(ts, it.tile - it.e * s.per_group, it.mt, it.nt);
-    it.row0 = bound[it.e];
-    it.cnt = bound[it.e + 1] - it.row0;
-  }
-  __device__ __forceinline__ bool next(const WgradParams& p, const WSched& s, const int* bound, WItem& it) {
-    if (unit_pending) {
-      unit_pending = false;
-      it.tile = s.tiles - s.split_tiles + cluster / s.splits;
-      fill(p, s, bound, it);
-      const int kbn = (it.cnt + kBK - 1) / kBK, piece = cluster % s.splits;
-      it.kb0 = static_cast<int>(static_cast<long long>(piece) * kbn / s.splits);
-      it.kb1 = static_cast<int>(static_cast<long long>(piece + 1) * kbn / s.splits);
-      it.unit = cluster;
-      return true;
+}
+
+__device__ __forceinline__ void store_chunk_tma(const CUtensorMap* map, uint32_t buf, int& turn, int lane, int c_dtype,
+                                                int col0, int row0, int e, const float (&v)[32]) {
+  auto next = [&]() { return buf + 2048u * (static_cast<uint32_t>(turn++) % kStageBufs); };
+  if (c_dtype == 0) {
+    uint32_t w[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(v[j]);
+    store_box(map, next(), lane, col0, row0, e, w);
+    store_box(map, next(), lane, col0 + 16, row0, e, w + 16);
+  } else {
+    uint32_t w[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      if (c_dtype == 1) {
+        const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+        w[k] = *reinterpret_cast<const uint32_t*>(&t);
+      } else {
+        const __half2 t = __floats2half2_rn(v[2 * k], v[2 * k + 1]);
+        w[k] = *reinterpret_cast<const uint32_t*>(&t);
+      }
     }
-    if (next_dp < s.tiles - s.split_tiles) {
-      it.tile = next_dp;
-      next_dp += s.P;
-      fill(p, s, bound, it);
-      it.kb0 = 0;
-      it.kb1 = (it.cnt + kBK - 1) / kBK;
-      it.unit = -1;
-      return true;
-    }
-    return false;
+    store_box(map, next(), lane, col0, row0, e, w);
   }
-};
+}
+
+// The same without tile stores (rows that are no whole number of 16-byte units): 16-byte
+// stores of 128 (FP32) or 64 (16-bit) consecutive bytes of a row, where a lane's own row
+// segments would fill half a 32-byte sector per store. 16-byte chunk j of a row sits at
+// j ^ (low row bits), so that neither side's accesses share a bank.
+__device__ __forceinline__ void store_chunk(const EpiArgs& e, uint8_t* buf, int lane, int row0, int col0,
+                                            const float (&v)[32]) {
+  const bool whole = col0 + 32 <= e.N;
+  if (e.c_dtype == 0) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // 16 rows at a time
+      __syncwarp();
+      const int r = lane - 16 * h;
+      if (r >= 0 && r < 16) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          reinterpret_cast<float4*>(buf)[r * 8 + (j ^ (r & 7))] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int rr = 4 * i + (lane >> 3), j = lane & 7, row = row0 + 16 * h + rr, col = col0 + 4 * j;
+        const float4 x = reinterpret_cast<const float4*>(buf)[rr * 8 + (j ^ (rr & 7))];
+        if (row < e.M) {
+          float* dst = static_cast<float*>(e.C) + static_cast<long long>(row) * e.ldc + col;
+          if (whole) {
+            *reinterpret_cast<float4*>(dst) = x;
+          } else {
+            const float y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (col + k < e.N) dst[k] = y[k];
+          }
+        }
+      }
+    }
+  } else {
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (e.c_dtype == 1) {
+          const __nv_bfloat162 t = __floats2bfloat162_rn(v[8 * j + 2 * k], v[8 * j + 2 * k + 1]);
+          w[k] = *reinterpret_cast<const uint32_t*>(&t);
+        } else {
+          const __half2 t = __floats2half2_rn(v[8 * j + 2 * k], v[8 * j + 2 * k + 1]);
+          w[k] = *reinterpret_cast<const uint32_t*>(&t);
+        }
+      }
+      reinterpret_cast<uint4*>(buf)[lane * 4 + (j ^ ((lane >> 1) & 3))] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int rr = 8 * i + (lane >> 2), j = lane & 3, row = row0 + rr, col = col0 + 8 * j;
+      const uint4 x = reinterpret_cast<const uint4*>(buf)[rr * 4 + (j ^ ((rr >> 1) & 3))];
+      if (row < e.M) {
+        uint16_t* dst = static_cast<uint16_t*>(e.C) + static_cast<long long>(row) * e.ldc + col;
+        if (whole) {
+          *reinterpret_cast<uint4*>(dst) = x;
+        } else {
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (col + k < e.N) dst[k] = static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1)));
+        }
+      }
+    }
+  }
+}
 }  // namespace
 
-__global__ void __launch_bounds__(kThreads, 1)
+// 128 registers: what is left of the register file holds a CTA of the bias kernel.
+__global__ void __maxnreg__(128)
     gemm_ragged_wgrad_kernel(const __grid_constant__ WgradMaps maps, const __grid_constant__ WgradParams p) {
   constexpr int SLOT = 128 * kTileN;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* smem_gen = smem_raw + (smem_base - smem_u32(smem_raw));
-  const uint32_t bar_base = smem_base + kStages * kStageBytes;
+  uint8_t* staging = smem_gen + kStages * kStageBytes;
+  const uint32_t ring_base = smem_base + kStages * kStageBytes + kEpiWarps * kStageWarpBytes;
+  const uint32_t bar_base = ring_base + kRing * kRingEntryBytes;
   auto full_bar = [&](int s) { return bar_base + 8u * s; };
   auto empty_bar = [&](int s) { return bar_base + 8u * (kStages + s); };
   auto tfull_bar = [&](int b) { return bar_base + 8u * (2 * kStages + b); };
   auto tempty_bar = [&](int b) { return bar_base + 8u * (2 * kStages + 2 + b); };
-  const uint32_t drain_bar = bar_base + 8u * (2 * kStages + 4);
-  uint8_t* misc = smem_gen + kStages * kStageBytes + 8 * (2 * kStages + 5);
+  const uint32_t drain_bar = bar_base + 8u * (2 * kStages + 4), epi_bar = bar_base + 8u * (2 * kStages + 5);
+  const uint32_t rfull_bar = epi_bar + 8u, rempty_bar = rfull_bar + 8u * kRing;
+  uint8_t* misc = smem_gen + kStages * kStageBytes + kEpiWarps * kStageWarpBytes + kRing * kRingEntryBytes + 8 * kBars;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 4);
   volatile int* reduce_flag = reinterpret_cast<volatile int*>(misc + 8);
   int* bound = reinterpret_cast<int*>(misc + 16);  // [E + 1]
-  int* tile0 = bound + p.E + 1;                    // [E + 1], unused here
+  int* order = bound + p.E + 1;                    // [E] experts, most rows first
 
   const uint32_t warp = warp_id(), lane = lane_id();
   const uint32_t rank = cluster_ctarank();
@@ -123,6 +229,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(tempty_bar(b), 2 * kEpiWarps);
     }
     mbar_init(drain_bar, 1);
+    mbar_init(epi_bar, kEpiWarps);
+    for (int s = 0; s < kRing; ++s) {
+      mbar_init(rfull_bar + 8 * s, 1);
+      mbar_init(rempty_bar + 8 * s, ring_readers(kEpiWarps));
+    }
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -130,9 +241,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc_pair(smem_u32(const_cast<uint32_t*>(tmem_slot)), kTcols);
     tmem_relinquish_pair();
   }
-  pdl_launch_dependents();
   pdl_wait();
-  if (warp == 3) build_group_table(p.offsets, p.E, p.T, 256, lane, bound, tile0);
+  pdl_launch_dependents();  // after the wait: the bias kernel relies on what precedes this launch
+  if (warp == 3) group_bounds(p.offsets, p.E, p.T, lane, bound);
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.E; e += kThreads) {
+    int rank_e = e;
+    if (p.E <= kSortGroups) {
+      const int cnt = bound[e + 1] - bound[e];
+      rank_e = 0;
+      for (int j = 0; j < p.E; ++j) {
+        const int c = bound[j + 1] - bound[j];
+        rank_e += c > cnt || (c == cnt && j < e);
+      }
+    }
+    order[rank_e] = e;
+  }
   tc_fence_before();
   __syncthreads();
   cluster_sync();
@@ -144,24 +268,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   s.per_group = p.m_tiles * p.n_tiles;
   s.tiles = s.per_group * p.E;
   s.P = static_cast<int>(gridDim.x >> 1);
-  {
-    // The last wave's R tiles are split when each piece keeps at least 8 blocks.
-    const int R = s.tiles % s.P;
-    s.split_tiles = 0;
-    s.splits = 1;
-    if (R > 0) {
-      int min_kb = 1 << 30;
-      for (int e = (s.tiles - R) / s.per_group; e < p.E; ++e) {
-        const int kb = (bound[e + 1] - bound[e] + kBK - 1) / kBK;
-        min_kb = kb < min_kb ? kb : min_kb;
-      }
-      const int S = min(s.P / R, min_kb / 8);
-      if (S >= 2) {
-        s.split_tiles = R;
-        s.splits = S;
-      }
-    }
-  }
+  s.splits = max(1, s.P / s.tiles);
+  const bool drawn = s.tiles > s.P;
+  Ring ring{ring_base, rfull_bar, rempty_bar, 0};
 
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
@@ -169,10 +278,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 0;
     long long issued = 0;
     bool ok = true;
-    WIter wi;
-    wi.init(s, cluster);
-    WItem it;
-    while (ok && wi.next(p, s, bound, it)) {
+    RingItem it{-1, 0, 0, 0, 0, 0, 0, 0};
+    if (rank == 0) {
+      // Drawn: tile `cluster`; else piece cluster % splits of tile cluster / splits.
+      const int t = cluster / s.splits, piece = cluster % s.splits;
+      if (t < s.tiles) {
+        it = resolve(p, s, bound, order, t);
+        const int n = pieces_of(s, it.kb1);
+        const long long kbn = it.kb1;
+        if (piece < n) {
+          it.kb0 = static_cast<int>(piece * kbn / n);
+          it.kb1 = static_cast<int>((piece + 1) * kbn / n);
+        } else {
+          it.e = -1;
+        }
+      }
+      ok = ring.publish(it, abort_flag, limit) && it.e >= 0;
+    } else {
+      ok = ring.take(it, abort_flag, limit);
+    }
+    while (ok) {
+      unsigned ticket = 0;
+      if (rank == 0 && drawn && lane == 0) ticket = draw_ticket(p.ticket, p.ticket_gen, s.P, s.tiles);
+      RingItem next{-1, 0, 0, 0, 0, 0, 0, 0};
+      // As in gemm_ragged.cu, the next tile is published while this one's loads are under way.
+      auto handover = [&]() {
+        if (rank != 0) return true;
+        if (drawn) {
+          ticket = __shfl_sync(0xffffffffu, ticket, 0);
+          if (ticket < static_cast<unsigned>(s.tiles)) next = resolve(p, s, bound, order, static_cast<int>(ticket));
+        }
+        return ring.publish(next, abort_flag, limit);
+      };
+      const int k_next = min(it.kb1 - 1, it.kb0 + kStages - 1);
       const int a_col = it.mt * 256 + static_cast<int>(rank) * 128;
       const int d_col = it.nt * kTileN + static_cast<int>(rank) * 128;
       for (int kb = it.kb0; kb < it.kb1; ++kb) {
@@ -190,8 +328,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_2d_pair(dst + kOpBytes, &maps.d[box], leader_full, d_col, row);
             tma_load_2d_pair(dst + kOpBytes + kBK * 128, &maps.d[box], leader_full, d_col + 64, row);
           };
-          const int row = it.row0 + kb * kBK;
-          const int valid = it.cnt - kb * kBK;
+          const int row = it.row + kb * kBK;
+          const int valid = it.nrow - kb * kBK;
           if (valid >= kBK) {
             load(0, 0, row);
           } else {
@@ -213,9 +351,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         ++issued;
         if (++stage == kStages) { stage = 0; phase ^= 1u; }
+        if (kb == k_next && !handover()) { ok = false; break; }
+      }
+      if (ok && it.kb0 == it.kb1) ok = handover();  // an expert without rows
+      if (!ok) break;
+      if (rank == 0) {
+        it = next;
+        ok = it.e >= 0;
+      } else {
+        ok = ring.take(it, abort_flag, limit);
       }
     }
-    if (!ok && rank == 0 && lane == 0) {
+    if (*abort_flag != 0 && rank == 0 && lane == 0) {
       int st = stage;
       uint32_t ph = phase;
       volatile int no_abort = 0;
@@ -230,17 +377,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 0;
     int local = 0;
     bool ok = true;
-    WIter wi;
-    wi.init(s, cluster);
-    WItem it;
-    while (ok && wi.next(p, s, bound, it)) {
-      if (it.kb1 == it.kb0) continue;  // an expert without rows: the epilogue writes zeros
+    RingItem it;
+    ok = ring.take(it, abort_flag, limit);
+    while (ok) {
+      const int kb0 = it.kb0, kb1 = it.kb1;
+      if (kb1 == kb0) {  // an expert without rows: the epilogue writes zeros
+        ok = ring.take(it, abort_flag, limit);
+        continue;
+      }
       const int acc = local & 1;
       const uint32_t acc_phase = (local >> 1) & 1;
       if (!__all_sync(0xffffffffu, mbar_wait(tempty_bar(acc), acc_phase ^ 1u, abort_flag, limit))) break;
       tc_fence_after();
       const uint32_t d_tmem = tmem_base + acc * kTileN;
-      for (int kb = it.kb0; kb < it.kb1; ++kb) {
+      bool more = true;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (kb == kb1 - 1) more = ring.take(it, abort_flag, limit);  // behind the MMAs in flight
         if (!__all_sync(0xffffffffu, mbar_wait(full_bar(stage), phase, abort_flag, limit))) { ok = false; break; }
         tc_fence_after();
         const uint32_t sa = smem_base + stage * kStageBytes;
@@ -248,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < kBK / 16; ++k)
             umma_f16_pair(d_tmem, operand_desc<128, kBK>(sa, 1, k), operand_desc<128, kBK>(sa + kOpBytes, 1, k),
-                          p.idesc, (kb > it.kb0 || k > 0) ? 1u : 0u);
+                          p.idesc, (kb > kb0 || k > 0) ? 1u : 0u);
           umma_commit_pair(empty_bar(stage), 0x3);
         }
         __syncwarp();
@@ -258,6 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (elect_one()) umma_commit_pair(tfull_bar(acc), 0x3);
       __syncwarp();
       ++local;
+      ok = more;
     }
     if (elect_one()) umma_commit_pair(drain_bar, 0x1);
     __syncwarp();
@@ -270,75 +423,76 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_addr = static_cast<uint32_t>(q * 32) << 16;
     const int epi_tid = threadIdx.x - kEpiWarp0 * 32;
     const int c_base = ((warp - kEpiWarp0) >> 2) * kEpiCols;
-    int local = 0;
-    bool dead = false;
-    WIter wi;
-    wi.init(s, cluster);
-    WItem it;
-    while (wi.next(p, s, bound, it)) {
+    uint8_t* buf = staging + (warp - kEpiWarp0) * kStageWarpBytes;
+    EpiBarrier epi{epi_bar, 0};
+    int local = 0, turn = 0;
+    RingItem it;
+    while (ring.take(it, abort_flag, limit)) {
       char* out = static_cast<char*>(p.C) + static_cast<long long>(it.e) * p.stride_c * (p.c_dtype == 0 ? 4 : 2);
       const EpiArgs e{p.K, p.N, nullptr, 0, 0, out, p.c_dtype, p.ldc};
-      const int row = it.mt * 256 + static_cast<int>(rank) * 128 + r_local;
+      const int row0 = it.mt * 256 + static_cast<int>(rank) * 128 + q * 32;
       const int col0 = it.nt * kTileN + c_base;
-      if (it.kb1 == it.kb0) {
+      auto emit = [&](int c, const float(&v)[32]) {
+        const int col = col0 + c * 32;
+        if (row0 >= p.K || col >= p.N) return;
+        if (p.tma_store) store_chunk_tma(&maps.c, smem_u32(buf), turn, static_cast<int>(lane), p.c_dtype, col, row0, it.e, v);
+        else store_chunk(e, buf, static_cast<int>(lane), row0, col, v);
+      };
+      if (it.kb1 == it.kb0) {  // an expert without rows
         float v[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = 0.0f;
 #pragma unroll 1
-        for (int c = 0; c < kEpiCols / 32; ++c) epi_store_row32(e, row, col0 + c * 32, v);
+        for (int c = 0; c < kEpiCols / 32; ++c) emit(c, v);
         continue;
       }
       const int acc = local & 1;
       const uint32_t acc_phase = (local >> 1) & 1;
-      if (!dead) dead = !mbar_wait(tfull_bar(acc), acc_phase, abort_flag, limit);
-      dead = __any_sync(0xffffffffu, dead);
+      if (!__all_sync(0xffffffffu, mbar_wait(tfull_bar(acc), acc_phase, abort_flag, limit))) break;
       const uint32_t tacc = tmem_base + lane_addr + acc * kTileN + c_base;
-      const bool split = it.unit >= 0;
-      float* my_slot = split ? p.slots + (static_cast<size_t>(it.unit) * 2 + rank) * SLOT : nullptr;
-      if (!dead) {
-        tc_fence_after();
+      const int n = s.splits > 1 ? pieces_of(s, (it.nrow + kBK - 1) / kBK) : 1;
+      float* my_slot = p.slots + (static_cast<size_t>(cluster) * 2 + rank) * SLOT;
+      tc_fence_after();
 #pragma unroll 1
-        for (int c = 0; c < kEpiCols / 32; ++c) {
-          uint32_t r[32];
-          tmem_ld_32x32b_x32_sync(tacc + c * 32, r);
-          float v[32];
+      for (int c = 0; c < kEpiCols / 32; ++c) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32_sync(tacc + c * 32, r);
+        float v[32];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-          if (split) slot_store<32>(my_slot, r_local, c_base + c * 32, v);
-          else epi_store_row32(e, row, col0 + c * 32, v);
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
+        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+        if (n > 1) slot_store<32>(my_slot, r_local, c_base + c * 32, v);
+        else emit(c, v);
       }
-      if (split) {
-        const int r_tail = it.tile - (s.tiles - s.split_tiles);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(tempty_bar(acc), 0));
+      if (n > 1) {
         __threadfence();
-        named_barrier_sync(1, kEpiThreads);
-        if (epi_tid == 0) {
-          const bool any_dead = *abort_flag != 0;
-          const int old = any_dead ? -1 : counter_arrive(p.counters + r_tail * 2 + rank, p.gen, s.splits);
-          *reduce_flag = (!any_dead && old == s.splits - 1);
-        }
-        named_barrier_sync(1, kEpiThreads);
+        if (!epi.sync(abort_flag, limit)) break;
+        if (epi_tid == 0) *reduce_flag = counter_arrive(p.counters + it.tile * 2 + rank, p.gen, n) == n - 1;
+        if (!epi.sync(abort_flag, limit)) break;
         if (*reduce_flag) {
           __threadfence();
+          const float* first = p.slots + (static_cast<size_t>(it.tile) * s.splits * 2 + rank) * SLOT;
 #pragma unroll 1
           for (int c = 0; c < kEpiCols / 32; ++c) {
             float v[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = 0.0f;
 #pragma unroll 1
-            for (int pc = 0; pc < s.splits; ++pc)
-              slot_accumulate<32>(p.slots + ((static_cast<size_t>(r_tail) * s.splits + pc) * 2 + rank) * SLOT, r_local,
-                                  c_base + c * 32, v);
-            epi_store_row32(e, row, col0 + c * 32, v);
+            for (int pc = 0; pc < n; pc += 2) {
+              const float* src = first + static_cast<size_t>(pc) * 2 * SLOT;
+              if (pc + 1 < n) slot_accumulate2<32>(src, src + 2 * SLOT, r_local, c_base + c * 32, v);
+              else slot_accumulate<32>(src, r_local, c_base + c * 32, v);
+            }
+            emit(c, v);
           }
         }
-        named_barrier_sync(1, kEpiThreads);
+        if (!epi.sync(abort_flag, limit)) break;  // reduce_flag has been read
       }
       ++local;
     }
+    if (lane == 0) bulk_wait_group<0>();  // this warp's tile stores have landed
   }
 
   tc_fence_before();
@@ -349,55 +503,73 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 namespace {
-// Column sums of one expert's rows of D: a CTA takes 64 columns, warp w the rows w, w + 8,
-// ..; the eight partial sums are added in warp order (deterministic).
+// Column sums of one expert's rows of D: a CTA takes 64 columns, 8 to a thread, and thread
+// row r the rows r, r + 32, ..; the partial sums are added in a fixed order (deterministic).
+// D's rows are read with 16-byte loads, four in flight per thread.
+//
+// Runs beside the weight-gradient kernel, which is launched just before it, lets it start
+// once its own CTAs have passed their dependency wait (all earlier work is then complete),
+// and leaves it registers and shared memory on every SM. CTA 0's wait at the end keeps this
+// kernel alive until that one is complete, so later work on the stream finds both done.
 template <bool BF16>
 __global__ void __launch_bounds__(256) ragged_dbias_kernel(const uint16_t* __restrict__ D, long long ldd, int T, int N,
-                                                           const int* __restrict__ offsets, float* __restrict__ db) {
-  __shared__ int sh_bound[2][8];
+                                                           const int* __restrict__ offsets, float* __restrict__ db,
+                                                           int beside) {
+  __shared__ int sh_bound[8];
   __shared__ float part[8][64];
-  pdl_launch_dependents();
-  pdl_wait();
+  if (!beside) pdl_wait();
   const int e = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // Bounds as in the group table: offsets clamped to [0, T] and to their running maximum.
+  // Bounds as in group_bounds: offsets clamped to [0, T] and to their running maximum.
   int lo = 0;
   for (int i = threadIdx.x; i <= e; i += 256) lo = max(lo, min(max(offsets[i], 0), T));
   lo = __reduce_max_sync(0xffffffffu, lo);
-  if (lane == 0) sh_bound[0][warp] = lo;
+  if (lane == 0) sh_bound[warp] = lo;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < 8; ++w) lo = max(lo, sh_bound[0][w]);
+  for (int w = 0; w < 8; ++w) lo = max(lo, sh_bound[w]);
   const int hi = max(lo, min(max(offsets[e + 1], 0), T));
-  const int col = blockIdx.x * 64 + 2 * lane;
-  float s0 = 0.0f, s1 = 0.0f;
-  auto add = [&](uint32_t w) {
-    float2 f;
-    if constexpr (BF16) f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
-    else f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-    s0 += f.x;
-    s1 += f.y;
+  const int r = threadIdx.x >> 3, col = blockIdx.x * 64 + 8 * (threadIdx.x & 7);
+  float s[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s[j] = 0.0f;
+  auto value = [](uint32_t bits) {
+    if constexpr (BF16) return __uint_as_float(bits << 16);
+    else return __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
   };
-  if (col + 1 < N) {
-#pragma unroll 8
-    for (int t = lo + warp; t < hi; t += 8)
-      add(__ldg(reinterpret_cast<const unsigned int*>(D + static_cast<long long>(t) * ldd + col)));
+  if (col + 8 <= N) {
+#pragma unroll 4
+    for (int t = lo + r; t < hi; t += 32) {
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(D + static_cast<long long>(t) * ldd + col));
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] += value((j & 1) ? w[j >> 1] >> 16 : w[j >> 1] & 0xffffu);
+    }
   } else if (col < N) {
-    for (int t = lo + warp; t < hi; t += 8) add(D[static_cast<long long>(t) * ldd + col]);
+    for (int t = lo + r; t < hi; t += 32)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (col + j < N) s[j] += value(D[static_cast<long long>(t) * ldd + col + j]);
   }
-  part[warp][2 * lane] = s0;
-  part[warp][2 * lane + 1] = s1;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    s[j] += __shfl_xor_sync(0xffffffffu, s[j], 8);
+    s[j] += __shfl_xor_sync(0xffffffffu, s[j], 16);
+    if (lane < 8) part[warp][8 * lane + j] = s[j];
+  }
   __syncthreads();
   const int c = threadIdx.x, n = blockIdx.x * 64 + c;
   if (c < 64 && n < N) {
-    float s = 0.0f;
+    float sum = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) s += part[w][c];
-    db[static_cast<long long>(e) * N + n] = s;
+    for (int w = 0; w < 8; ++w) sum += part[w][c];
+    db[static_cast<long long>(e) * N + n] = sum;
   }
+  pdl_launch_dependents();
+  if (beside && blockIdx.x == 0 && blockIdx.y == 0) pdl_wait();
 }
 
-constexpr int kSmem = 1024 + kStages * kStageBytes + 8 * (2 * kStages + 5) + 16 +
-                      2 * (kRaggedMaxGroups + 1) * static_cast<int>(sizeof(int));
+constexpr int kSmem = 1024 + kStages * kStageBytes + kEpiWarps * kStageWarpBytes + kRing * kRingEntryBytes + 8 * kBars +
+                      16 + 2 * (kRaggedMaxGroups + 1) * static_cast<int>(sizeof(int));
 static_assert(kSmem <= 232448, "shared memory budget");
 
 cudaLaunchConfig_t config(int clusters, cudaStream_t stream, cudaLaunchAttribute* attr) {
@@ -445,7 +617,7 @@ cudaError_t launch_gemm_ragged_wgrad(const WgradMaps& m, const WgradParams& p, i
 }
 
 cudaError_t launch_ragged_dbias(const void* D, bool bf16, long long ldd, int T, int N, const int* offsets, int E,
-                                float* db, cudaStream_t stream) {
+                                float* db, bool after_wgrad, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   cfg.gridDim = dim3((N + 63) / 64, E, 1);
@@ -454,8 +626,9 @@ cudaError_t launch_ragged_dbias(const void* D, bool bf16, long long ldd, int T, 
   cfg.attrs = attr;
   add_pdl_attr(cfg, attr);
   const uint16_t* d = static_cast<const uint16_t*>(D);
-  const cudaError_t e = bf16 ? cudaLaunchKernelEx(&cfg, ragged_dbias_kernel<true>, d, ldd, T, N, offsets, db)
-                             : cudaLaunchKernelEx(&cfg, ragged_dbias_kernel<false>, d, ldd, T, N, offsets, db);
+  const int beside = after_wgrad && cfg.numAttrs > 0 ? 1 : 0;  // without programmatic launch: in stream order
+  const cudaError_t e = bf16 ? cudaLaunchKernelEx(&cfg, ragged_dbias_kernel<true>, d, ldd, T, N, offsets, db, beside)
+                             : cudaLaunchKernelEx(&cfg, ragged_dbias_kernel<false>, d, ldd, T, N, offsets, db, beside);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

@@ -16,6 +16,14 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
+// As tma_store_2d, through a 3-D tensor map.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int32_t c0, int32_t c1, int32_t c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+
 // D[tmem] (+)= A * B over a CTA pair, signed 8-bit integers, int32 accumulate (K = 32).
 __device__ __forceinline__ void umma_i8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                              uint32_t accumulate) {
@@ -38,33 +46,40 @@ __device__ __forceinline__ int tile_width(int cnt, int tn) {
   return nt == 0 ? 32 : ((cnt + nt - 1) / nt + 31) & ~31;
 }
 
-// Group table by one warp: bound[e] .. bound[e+1] are the rows of group e, tile0[e] its
-// first token tile. Offsets are clamped to [0, T] and to their running maximum, so that no
-// offset makes two groups write one row or any row outside C.
-__device__ __forceinline__ void build_group_table(const int* offsets, int E, int T, int tn, uint32_t lane, int* bound,
-                                                  int* tile0) {
-  auto clamp_t = [&](int v) { return v < 0 ? 0 : (v > T ? T : v); };
-  int run = offsets == nullptr ? 0 : clamp_t(offsets[0]);
-  int tiles = 0;
-  if (lane == 0) {
-    bound[0] = run;
-    tile0[0] = 0;
+// Row bounds by one warp: bound[e] .. bound[e+1] are the rows of group e. Offsets are clamped
+// to [0, T] and to their running maximum, so that no offset makes two groups write one row
+// or any row outside the matrices.
+__device__ __forceinline__ void group_bounds(const int* offsets, int E, int T, uint32_t lane, int* bound) {
+  if (offsets == nullptr) {  // one group
+    if (lane < 2) bound[lane] = lane == 0 ? 0 : T;
+    return;
   }
-  for (int base = 0; base < E; base += 32) {
+  auto clamp_t = [&](int v) { return v < 0 ? 0 : (v > T ? T : v); };
+  int run = 0;
+  for (int base = 0; base <= E; base += 32) {
     const int i = base + static_cast<int>(lane);
-    int v = i < E ? (offsets == nullptr ? T : clamp_t(offsets[i + 1])) : 0;
+    int v = i <= E ? clamp_t(offsets[i]) : 0;
     v = v > run ? v : run;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int o = __shfl_up_sync(0xffffffffu, v, d);
       if (static_cast<int>(lane) >= d && o > v) v = o;
     }
-    int prev = __shfl_up_sync(0xffffffffu, v, 1);
-    if (lane == 0) prev = run;
-    const int cnt = v - prev;
+    if (i <= E) bound[i] = v;
+    run = __shfl_sync(0xffffffffu, v, 31);
+  }
+}
+
+// First token tile of every group by one warp (after group_bounds): tile0[E] is their number.
+__device__ __forceinline__ void group_tiles(const int* bound, int E, int cap, uint32_t lane, int* tile0) {
+  int tiles = 0;
+  if (lane == 0) tile0[0] = 0;
+  for (int base = 0; base < E; base += 32) {
+    const int i = base + static_cast<int>(lane);
     int nt = 0;
-    if (cnt > 0) {
-      const int w = tile_width(cnt, tn);
+    if (i < E) {
+      const int cnt = bound[i + 1] - bound[i];
+      const int w = tile_width(cnt, cap);
       nt = (cnt + w - 1) / w;
     }
 #pragma unroll
@@ -72,11 +87,7 @@ __device__ __forceinline__ void build_group_table(const int* offsets, int E, int
       const int o = __shfl_up_sync(0xffffffffu, nt, d);
       if (static_cast<int>(lane) >= d) nt += o;
     }
-    if (i < E) {
-      bound[i + 1] = v;
-      tile0[i + 1] = tiles + nt;
-    }
-    run = __shfl_sync(0xffffffffu, v, 31);
+    if (i < E) tile0[i + 1] = tiles + nt;
     tiles += __shfl_sync(0xffffffffu, nt, 31);
   }
 }

@@ -11,9 +11,11 @@ constexpr int kRaggedMaxGroups = 1024;  // the group table sits in shared memory
 // Tensor maps of one call. w: the weights as a 3-D tensor (box 64 N x 64 K elements of one
 // expert when N is contiguous, else 128 bytes of K x 128 N). x[i]: the activation rows,
 // boxes of 128 bytes of K x (64 >> i) rows.
+// c: the output, boxes of 32 columns x 32 (16-bit) or 16 (FP32) rows.
 struct RaggedMaps {
   CUtensorMap w;
   CUtensorMap x[3];
+  CUtensorMap c;
 };
 
 struct RaggedParams {
@@ -29,17 +31,21 @@ struct RaggedParams {
   long long ldc;
   const float* sa;          // int8: [T] row scales
   const float* sb;          // int8: [E][N] column scales
-  float* slots;             // partial tiles: [clusters][2][2 ranks][TN][128] 32-bit words
+  float* slots;             // partial tiles: [clusters][2][2 ranks][slot_words]
   unsigned long long* counters;  // [clusters][2] arrival counters of split tiles
   unsigned long long gen;
+  unsigned long long* ticket;    // draw_ticket's word
+  uint32_t ticket_gen;
+  int slot_words;           // 32-bit words of one CTA's partial tile: 128 x its most rows
+  int choose;               // estimate the tile height (else the highest)
+  int tma_store;            // maps.c may be used
+  int force_cap;            // rows of a tile at most (0: by estimate)
+  int force_sched;          // 1: whole tiles, 2: cut along K, 0: by estimate
   unsigned long long wait_limit_cycles;
 };
 
-// narrow: token tiles of at most 64 rows (else 256).
-cudaError_t launch_gemm_ragged(const RaggedMaps& m, const RaggedParams& p, bool i8, bool narrow, int clusters,
-                               cudaStream_t stream);
+cudaError_t launch_gemm_ragged(const RaggedMaps& m, const RaggedParams& p, bool i8, int clusters, cudaStream_t stream);
 int ragged_max_clusters();
-inline int ragged_tile_tokens(bool narrow) { return narrow ? 64 : 256; }
 unsigned take_error_word_ragged();
 
 // Weight gradients (gemm_ragged_wgrad.cu). Boxes of 64 columns x (64 >> i) rows of A and D.
@@ -47,6 +53,7 @@ constexpr int kWgradBoxes = 7;
 struct WgradMaps {
   CUtensorMap a[kWgradBoxes];
   CUtensorMap d[kWgradBoxes];
+  CUtensorMap c;  // dB, boxes of 64 bytes of a row x 32 rows
 };
 
 struct WgradParams {
@@ -56,17 +63,20 @@ struct WgradParams {
   uint32_t idesc;
   void* C;
   int c_dtype;
+  int tma_store;            // maps.c may be used
   long long ldc, stride_c;  // elements between rows / experts of dB
   float* slots;             // split tiles: [clusters][2 ranks][128][256] partials
   unsigned long long* counters;  // [clusters][2]
   unsigned long long gen;
+  unsigned long long* ticket;    // draw_ticket's word
+  uint32_t ticket_gen;
   unsigned long long wait_limit_cycles;
 };
 
 cudaError_t launch_gemm_ragged_wgrad(const WgradMaps& m, const WgradParams& p, int clusters, cudaStream_t stream);
 int wgrad_max_clusters();
 cudaError_t launch_ragged_dbias(const void* D, bool bf16, long long ldd, int T, int N, const int* offsets, int E,
-                                float* db, cudaStream_t stream);
+                                float* db, bool after_wgrad, cudaStream_t stream);
 unsigned take_error_word_wgrad();
 
 // Row quantiser (quant_int8.cu): X [M][K] of dtype, rows ld_bytes apart (16-byte aligned).

@@ -1,0 +1,145 @@
+// Tile scheduling of the ragged products: how the clusters of one launch share tiles whose
+// number and cost only the device knows.
+//
+// With more tiles than clusters, every cluster starts on tile c and then draws the next
+// tile from a counter in the workspace, so clusters that got short tiles take more of them
+// (an expert's rows decide a tile's cost; round-robin left SMs idle for 37% of a launch with
+// log-normal expert sizes). Tiles are drawn in raster order, so the tiles in flight are
+// neighbours and share operands in L2. The producer warp of the pair's rank-0 CTA draws
+// ticket i + 1 when it starts tile i (the atomic's latency hides behind the tile's loads)
+// and publishes the resolved tile to both CTAs through a ring of entries in their shared
+// memory; the other warps wait for entries and release them.
+#pragma once
+
+#include "sm100.cuh"
+
+namespace smg {
+
+constexpr int kRing = 4;             // published tiles that some warp may still have to read
+constexpr int kRingEntryBytes = 32;
+
+// One piece of work: K blocks [kb0, kb1) of a tile. stop: no more work.
+struct RingItem {
+  int e;           // group; -1: stop
+  int row, nrow;   // first row and rows of the tile (wgrad: of the group)
+  int mt, nt;      // tile coordinates (products: nt = feature tile)
+  int kb0, kb1;
+  int tile;        // tile number | (slot << 31)
+};
+
+__device__ __forceinline__ int ring_tile(const RingItem& it) { return it.tile & 0x7fffffff; }
+__device__ __forceinline__ int ring_slot(const RingItem& it) { return static_cast<unsigned>(it.tile) >> 31; }
+
+// Arms an mbarrier of any CTA of the cluster for `bytes` of asynchronous stores. Relaxed:
+// nothing is published with the arrival itself (see mbar_arrive_cluster_relaxed for what a
+// release at cluster scope costs).
+__device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t cluster_addr, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_addr),
+               "r"(bytes)
+               : "memory");
+}
+
+// Asynchronous 16-byte store to any CTA of the cluster, counted in bytes on its barrier.
+__device__ __forceinline__ void st_async_16(uint32_t cluster_addr, int a, int b, int c, int d, uint32_t cluster_bar) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(cluster_addr),
+      "r"(a), "r"(b), "r"(c), "r"(d), "r"(cluster_bar)
+      : "memory");
+}
+
+// The ring as one warp sees it. `entries`: this CTA's entries; full: this CTA's barriers (one
+// arrival and the entry's bytes); empty: the rank-0 CTA's barriers (every reading warp).
+struct Ring {
+  uint32_t entries, full, empty;
+  int pos;
+
+  __device__ __forceinline__ void advance() { ++pos; }
+  __device__ __forceinline__ uint32_t slot() const { return static_cast<uint32_t>(pos) % kRing; }
+  __device__ __forceinline__ uint32_t phase() const { return (static_cast<uint32_t>(pos) / kRing) & 1u; }
+
+  // Rank 0's producer warp: hands `it` to both CTAs (one elected lane writes).
+  __device__ __forceinline__ bool publish(const RingItem& it, volatile int* abort_flag, uint64_t limit) {
+    const uint32_t s = slot();
+    if (!__all_sync(0xffffffffu, mbar_wait(empty + 8 * s, phase() ^ 1u, abort_flag, limit))) return false;
+    if (elect_one()) {
+#pragma unroll
+      for (uint32_t r = 0; r < 2; ++r) {
+        const uint32_t bar = mapa_shared(full + 8 * s, r), dst = mapa_shared(entries + kRingEntryBytes * s, r);
+        mbar_arrive_expect_tx_cluster(bar, kRingEntryBytes);
+        st_async_16(dst, it.e, it.row, it.nrow, it.mt, bar);
+        st_async_16(dst + 16, it.nt, it.kb0, it.kb1, it.tile, bar);
+      }
+    }
+    __syncwarp();
+    advance();
+    return true;
+  }
+
+  // Every other warp: the next entry, released at once (it is copied to registers).
+  __device__ __forceinline__ bool take(RingItem& it, volatile int* abort_flag, uint64_t limit) {
+    const uint32_t s = slot();
+    if (!__all_sync(0xffffffffu, mbar_wait(full + 8 * s, phase(), abort_flag, limit))) return false;
+    const uint32_t a = entries + kRingEntryBytes * s;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(it.e), "=r"(it.row), "=r"(it.nrow), "=r"(it.mt)
+                 : "r"(a)
+                 : "memory");
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(it.nt), "=r"(it.kb0), "=r"(it.kb1), "=r"(it.tile)
+                 : "r"(a + 16)
+                 : "memory");
+    // The arrival's address depends on the loaded words, so it follows them; relaxed, since a
+    // release at cluster scope stalled every tile by ~1.3 us.
+    uint32_t zero;
+    asm volatile("and.b32 %0, %1, 0;" : "=r"(zero) : "r"(it.mt ^ it.tile));
+    zero = __reduce_or_sync(0xffffffffu, zero);
+    if (lane_id() == 0) mbar_arrive_cluster_relaxed(mapa_shared(empty + 8 * s + zero, 0));
+    advance();
+    return it.e >= 0;
+  }
+};
+
+// Arrivals per phase of an `empty` barrier: rank 0's MMA warp and both CTAs' epilogue warps,
+// and rank 1's producer.
+__host__ __device__ constexpr int ring_readers(int epi_warps) { return 2 * epi_warps + 2; }
+
+// Barrier of a CTA's epilogue warps whose wait is bounded (a stalled pipeline may leave some
+// of them without the tile the others are on): false when it was given up.
+struct EpiBarrier {
+  uint32_t bar, phase;
+  __device__ __forceinline__ bool sync(volatile int* abort_flag, uint64_t limit) {
+    __syncwarp();
+    if (lane_id() == 0) mbar_arrive(bar);
+    const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, phase, abort_flag, limit));
+    phase ^= 1u;
+    return ok;
+  }
+};
+
+// Next ticket of this launch. The word holds the call's generation (upper 32 bits) and the
+// next ticket; a word of another generation counts as not begun, so the workspace needs no
+// zeroing. Tickets start at `clusters` (tiles 0 .. clusters-1 are taken without one), and
+// each cluster draws until its ticket is past the last tile: the last such draw resets the
+// word, so that a captured call replays from the beginning.
+__device__ __forceinline__ unsigned draw_ticket(unsigned long long* word, uint32_t gen, unsigned clusters, unsigned tiles) {
+  unsigned long long cur = *reinterpret_cast<volatile unsigned long long*>(word);
+  unsigned t = 0xffffffffu;
+#pragma unroll 1
+  for (int i = 0; i < 4096; ++i) {
+    if (static_cast<uint32_t>(cur >> 32) == gen) {
+      t = static_cast<unsigned>(atomicAdd(word, 1ull));
+      break;
+    }
+    const unsigned long long prev =
+        atomicCAS(word, cur, (static_cast<unsigned long long>(gen) << 32) | (clusters + 1ull));
+    if (prev == cur) {
+      t = clusters;
+      break;
+    }
+    cur = prev;
+  }
+  if (t == tiles + clusters - 1) atomicExch(word, 0ull);
+  return t;
+}
+
+}  // namespace smg
