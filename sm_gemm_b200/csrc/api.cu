@@ -1190,11 +1190,23 @@ smgemm_status ragged_impl(const RaggedArgs& a, void* workspace, size_t workspace
   p.sb = a.sb;
   ragged_workspace(p, workspace, P);
   p.slot_words = 128 * rows;
-  const long long cap = env_ll(kKnobRaggedRows, 0);  // one of the kernel's tile heights, or 0
-  p.force_cap = cap == 256 || cap == 192 || cap == 128 || cap == 96 || cap == 64 || cap == 32 ? static_cast<int>(cap) : 0;
-  // One width fits all with T <= 32; with many tiles of the full height per cluster (were all
-  // rows one expert's) a lower height can only cost.
-  p.choose = a.T > 32 && (a.T / 256) * n_ft < 4 * static_cast<int64_t>(P) ? 1 : 0;
+  // Tile height: the full one, unless there may be so few tiles that lower ones fill the GPU
+  // better - then the kernel compares (for the one group of a dense product, this does).
+  const long long forced = env_ll(kKnobRaggedRows, 0);  // SMGEMM_RAGGED_ROWS: one of the heights
+  for (int cap = 256; cap >= 32; cap = next_cap(cap))
+    if (forced == cap) p.cap = cap;
+  if (p.cap == 0 && (a.T <= 32 || (std::min<int64_t>(a.E, a.T) + a.T / 256) * n_ft >= 3 * static_cast<int64_t>(P))) p.cap = 256;
+  if (p.cap == 0 && a.offsets == nullptr) {
+    unsigned best = 0xffffffffu;
+    for (int cap = 256; cap >= 32; cap = next_cap(cap)) {
+      const int w = tile_width(p.T, cap);
+      const unsigned c = wave_cycles((p.T + w - 1) / w * p.n_ft, w, P);
+      if (c < best) {
+        best = c;
+        p.cap = cap;
+      }
+    }
+  }
   p.force_sched = sched_mode() == SchedMode::kDP ? 1 : (sched_mode() == SchedMode::kSK ? 2 : 0);
   p.wait_limit_cycles = wait_limit();
   // The tile count depends on the offsets: launch as many clusters as the most tiles and

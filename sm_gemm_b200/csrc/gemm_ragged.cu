@@ -44,73 +44,33 @@ constexpr int kThreads = 32 * kEpiWarp0 + kEpiThreads;
 constexpr int kStageWarpBytes = 2048;  // epilogue transposition buffer per warp
 constexpr int kWBytes = 128 * 128;     // one CTA's weight tile of a stage: 128 features x 128 bytes of K
 
-// What the CTAs of a launch agree on, computed by each from the offsets.
-struct Plan {
-  int cap;          // rows of a tile at most
-  int tiles;        // of all groups and features
-  int width;        // widest tile of this call
-  int stream_k;     // static schedule with a split remainder instead of drawn tiles
-};
-
-// Tile heights to choose from: 256, 192, 128, 96, 64, 32 rows.
-constexpr int kNumCaps = 6;
-__device__ __forceinline__ int cap_of(int j) { return j < 2 ? 256 - 64 * j : 192 - 32 * j; }
-
-// Picks the tile height and the schedule, by one warp, from estimated cycles of the launch:
-// - one tile of w rows and kb K blocks: the MMA takes 2 w per block, the loads (128 x 128
-//   bytes of weights and 64 w bytes of rows per CTA, 64 bytes per cycle from L2) 256 + w,
-//   the longer for every w < 256; plus 700 for the tile's start and end;
-// - tiles drawn one by one: an even share plus on average half the longest tile for the
-//   last one; equal tiles need whole waves;
-// - cut along K: an even share plus the fix-up of a split tile (write, arrive, read back,
-//   epilogue: kFixup cycles, measured on narrow tiles);
-// - never faster than the active experts' weights come from HBM (9.6 cycles per 32 KB).
-// A lower cap has to be 2% better. With p.choose == 0 (T <= 32: one width; or so many tiles
-// that the highest is best) only the schedule is picked.
-constexpr float kFixup = 9000.0f;
-
-__device__ __forceinline__ Plan make_plan(const RaggedParams& p, const int* bound, int P, uint32_t lane) {
-  Plan pl{256, 0, 32, 0};
-  float best = 0.0f;
-  const float kb = static_cast<float>(p.kb_total), n_ft = static_cast<float>(p.n_ft);
-  const int first = p.force_cap != 0 ? (p.force_cap > 128 ? (256 - p.force_cap) / 64 : (192 - p.force_cap) / 32) : 0;
-  const int last = p.force_cap != 0 ? first : (p.choose ? kNumCaps - 1 : 0);
+// Tile height for groups that may have too few tiles at the full height, by one warp: the
+// cap with the least estimated cycles, waves x K blocks x (256 + w). A block of a tile of w
+// rows takes 256 + w cycles, since shared memory (128 bytes per cycle) bounds it: 16 KB of
+// weights and 64 w bytes of rows are written and read once per CTA (the MMA itself takes 2 w).
+__device__ __forceinline__ int choose_cap(const int* bound, int E, int n_ft, int P, uint32_t lane) {
+  int best = 256;
+  unsigned best_cycles = 0xffffffffu;
 #pragma unroll 1
-  for (int j = first; j <= last; ++j) {
-    const int cap = cap_of(j);
-    int tiles = 0, width = 32, active = 0;
-    unsigned rows = 0;  // summed 256 + w of the tiles, in units of 32
+  for (int cap = 256; cap >= 32; cap = next_cap(cap)) {
+    int tiles = 0, width = 32;
 #pragma unroll 1
-    for (int i = static_cast<int>(lane); i < p.E; i += 32) {
+    for (int i = static_cast<int>(lane); i < E; i += 32) {
       const int cnt = bound[i + 1] - bound[i];
       if (cnt <= 0) continue;
-      const int w = tile_width(cnt, cap), nt = (cnt + w - 1) / w;
-      tiles += nt;
-      active += 1;
+      const int w = tile_width(cnt, cap);
+      tiles += (cnt + w - 1) / w;
       width = max(width, w);
-      rows += static_cast<unsigned>(nt) * static_cast<unsigned>(8 + (w >> 5));
     }
     tiles = __reduce_add_sync(0xffffffffu, tiles);
-    if (tiles == 0) break;  // no rows at all
-    active = __reduce_add_sync(0xffffffffu, active);
     width = __reduce_max_sync(0xffffffffu, width);
-    rows = __reduce_add_sync(0xffffffffu, rows);
-    const float all = static_cast<float>(tiles) * n_ft;
-    const float sum = n_ft * (32.0f * kb * static_cast<float>(rows) + 700.0f * static_cast<float>(tiles));
-    const float longest = kb * static_cast<float>(256 + width) + 700.0f;
-    const float share = sum / static_cast<float>(P), hbm = static_cast<float>(active) * n_ft * kb * 9.6f;
-    float drawn = all <= static_cast<float>(P) ? longest
-                                               : fmaxf(share + 0.5f * longest, ceilf(all / static_cast<float>(P)) * (sum / all));
-    drawn = fmaxf(drawn, hbm);
-    const float split = fmaxf(share, hbm) + kFixup;
-    const int sk = p.force_sched == 2 || (p.force_sched == 0 && split < drawn);
-    const float t = sk ? split : drawn;
-    if (pl.tiles == 0 || t < 0.98f * best) {
-      best = t;
-      pl = Plan{cap, tiles * p.n_ft, width, sk};
+    const unsigned cycles = wave_cycles(tiles * n_ft, width, P);
+    if (cycles < best_cycles) {
+      best_cycles = cycles;
+      best = cap;
     }
   }
-  return pl;
+  return best;
 }
 
 // The tile with number t (whole, no slot).
@@ -172,19 +132,28 @@ __device__ __forceinline__ TileSched make_sched(int tiles, int kb, int P, int mi
   return s;
 }
 
-// 32 features (lanes) x 32 rows of C^T in registers -> C: scale, bias, activation, cast,
-// transposition through this warp's 2 KB buffer, 16-byte stores of whole row segments.
-// sb, b: the lane's column scale and bias; f0: the warp's first feature; row0: first row;
-// nrow: rows to store (<= 32).
+// Where a finished chunk goes: features f0 .. f0+31, rows row0 .. row0+nrow-1 of C.
+struct Chunk {
+  int f0, row0, nrow;
+};
+
+// Feature (0..31 of the warp's) of a thread's k-th column scale and bias: with 16-bit
+// output the thread holds fragments (features t / 4 + 8 k), with FP32 one feature, its lane.
+__device__ __forceinline__ int chunk_feature(int c_dtype, int lane, int k) {
+  return c_dtype == 0 ? lane : (lane >> 2) + 8 * k;
+}
+
+// FP32 output: lane = feature, r = its 32 rows. Scale, bias, activation, then 16 rows of 128
+// bytes at a time through the warp's 2 KB buffer.
 template <bool I8>
-__device__ __forceinline__ void emit_chunk(const RaggedParams& p, const CUtensorMap* tm_c, uint8_t* buf, int lane, float sb, float b, int f0,
-                                           int row0, int nrow, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void emit_f32(const RaggedParams& p, const CUtensorMap* tm_c, uint8_t* buf, int lane, float sb,
+                                         float b, const Chunk& ch, const uint32_t (&r)[32]) {
   float v[32];
   if (p.kb_total == 0) {  // no products: C = act(bias)
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] = 0.0f;
   } else if constexpr (I8) {
-    const float sa = lane < nrow ? __ldg(p.sa + row0 + lane) : 0.0f;
+    const float sa = lane < ch.nrow ? __ldg(p.sa + ch.row0 + lane) : 0.0f;
     // int32 -> FP32 rounds sums of 2^24 and more to nearest (relative error 2^-24).
 #pragma unroll
     for (int j = 0; j < 32; ++j)
@@ -193,8 +162,8 @@ __device__ __forceinline__ void emit_chunk(const RaggedParams& p, const CUtensor
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
   }
-  if (p.act != 0 && p.c_dtype == 0) {
-    // FP32 output: activation in double, one copy of the code (see epi_bias_act32_f64).
+  if (p.act != 0) {
+    // Activation in double, one copy of the code (see epi_bias_act32_f64).
 #pragma unroll 1
     for (int j = 0; j < 32; ++j) {
       const float y = __double2float_rn(act_apply_f64(static_cast<double>(v[0]) + static_cast<double>(b), p.act));
@@ -202,139 +171,177 @@ __device__ __forceinline__ void emit_chunk(const RaggedParams& p, const CUtensor
       for (int k = 0; k < 31; ++k) v[k] = v[k + 1];
       v[31] = y;
     }
-  } else {
-    if (p.bias != nullptr) {
+  } else if (p.bias != nullptr) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] += b;
-    }
-    if (p.act == 1) {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const float2 y = act_apply2(make_float2(v[2 * j], v[2 * j + 1]), 1);
-        v[2 * j] = y.x;
-        v[2 * j + 1] = y.y;
-      }
-    } else if (p.act == 2) {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const float2 y = act_apply2(make_float2(v[2 * j], v[2 * j + 1]), 2);
-        v[2 * j] = y.x;
-        v[2 * j + 1] = y.y;
-      }
-    }
+    for (int j = 0; j < 32; ++j) v[j] += b;
   }
-  const bool whole = f0 + 32 <= p.N;
-  // The buffer may still be read by this warp's last tile store.
-  if (lane == 0) bulk_wait_group_read<0>();
-  // Whole 32-row chunks leave as a TMA tile store (clipped to C's columns), so the warp does
-  // not wait for its stores; rows past the expert's end must stay as they are, so a last
-  // chunk is stored row by row.
-  const bool tma = p.tma_store && nrow == 32;
-  if (p.c_dtype == 0) {
-    float* C = static_cast<float*>(p.C);
+  float* C = static_cast<float*>(p.C);
+  const bool whole = ch.f0 + 32 <= p.N, tma = p.tma_store && ch.nrow == 32;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {  // 16 rows of 128 bytes at a time
-      if (h == 1 && lane == 0) bulk_wait_group_read<0>();
-      __syncwarp();
-      // 16-byte unit u of row j at u ^ (j & 7): the 128-byte swizzle of the store's map.
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        reinterpret_cast<float*>(buf)[j * 32 + (((lane >> 2) ^ (j & 7)) << 2) + (lane & 3)] = v[16 * h + j];
-      if (tma) {
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_2d(tm_c, smem_u32(buf), f0, row0 + 16 * h);
-          bulk_commit_group();
-        }
-        continue;
-      }
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = 4 * i + (lane >> 3), c = 4 * (lane & 7);
-        const float4 x = reinterpret_cast<const float4*>(buf)[row * 8 + ((lane & 7) ^ (row & 7))];
-        if (16 * h + row < nrow) {
-          float* dst = C + static_cast<long long>(row0 + 16 * h + row) * p.ldc + f0 + c;
-          if (whole) {
-            *reinterpret_cast<float4*>(dst) = x;
-          } else {
-            const float y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              if (f0 + c + q < p.N) dst[q] = y[q];
-          }
-        }
-      }
-    }
-  } else {
-    // Lane pairs exchange halves so that each 32-bit word holds two neighbouring features
-    // of one row: the even lane keeps row 2j, the odd lane row 2j + 1. 16-byte unit u of row
-    // j sits at u ^ ((j >> 1) & 3): the 64-byte swizzle of the store's map.
-    const bool odd = lane & 1;
+  for (int h = 0; h < 2; ++h) {
+    if (lane == 0) bulk_wait_group_read<0>();  // the buffer may still be read by the last tile store
     __syncwarp();
+    // 16-byte unit u of row j at u ^ (j & 7): the 128-byte swizzle of the store's map.
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const float give = odd ? v[2 * j] : v[2 * j + 1];
-      const float got = __shfl_xor_sync(0xffffffffu, give, 1);
-      const float lo = odd ? got : v[2 * j], hi = odd ? v[2 * j + 1] : got;
-      uint32_t w;
-      if (p.c_dtype == 1) {
-        const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
-        w = *reinterpret_cast<const uint32_t*>(&t);
-      } else {
-        const __half2 t = __floats2half2_rn(lo, hi);
-        w = *reinterpret_cast<const uint32_t*>(&t);
-      }
-      reinterpret_cast<uint32_t*>(buf)[(2 * j + (odd ? 1 : 0)) * 16 + (((lane >> 3) ^ (j & 3)) << 2) + ((lane >> 1) & 3)] = w;
-    }
+    for (int j = 0; j < 16; ++j)
+      reinterpret_cast<float*>(buf)[j * 32 + (((lane >> 2) ^ (j & 7)) << 2) + (lane & 3)] = v[16 * h + j];
     if (tma) {
       fence_proxy_async_shared();
       __syncwarp();
       if (lane == 0) {
-        tma_store_2d(tm_c, smem_u32(buf), f0, row0);
+        tma_store_2d(tm_c, smem_u32(buf), ch.f0, ch.row0 + 16 * h);
         bulk_commit_group();
       }
-      return;
+      continue;
     }
     __syncwarp();
-    uint16_t* C = static_cast<uint16_t*>(p.C);
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < 4; ++i) {
-      const int row = 8 * i + (lane >> 2), c = 8 * (lane & 3);
-      const uint4 x = reinterpret_cast<const uint4*>(buf)[row * 4 + ((lane & 3) ^ ((row >> 1) & 3))];
-      if (row < nrow) {
-        uint16_t* dst = C + static_cast<long long>(row0 + row) * p.ldc + f0 + c;
+      const int row = 4 * i + (lane >> 3), f = ch.f0 + 4 * (lane & 7);
+      const float4 x = reinterpret_cast<const float4*>(buf)[row * 8 + ((lane & 7) ^ (row & 7))];
+      if (16 * h + row < ch.nrow) {
+        float* dst = C + static_cast<long long>(ch.row0 + 16 * h + row) * p.ldc + f;
         if (whole) {
-          *reinterpret_cast<uint4*>(dst) = x;
+          *reinterpret_cast<float4*>(dst) = x;
         } else {
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          const float y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            if (f0 + c + q < p.N) dst[q] = static_cast<uint16_t>(w[q >> 1] >> (16 * (q & 1)));
+          for (int q = 0; q < 4; ++q)
+            if (f + q < p.N) dst[q] = y[q];
         }
       }
     }
   }
 }
 
-// Partial sums of a split tile: FP32 partials add as floats, int32 partials as integers.
-// Two contributors' loads are in flight before the first add.
-__device__ __forceinline__ void slot_load32(const float* slot, int r_local, int col0, uint4 (&t)[8]) {
-  const uint4* s4 = reinterpret_cast<const uint4*>(slot);
+// 16-bit output: r[16 h + 4 c + k] = fragment (feature 16 h + 8 (k / 2) + lane / 4, row
+// 8 c + 2 (lane % 4) + (k & 1)), so that neighbouring rows pack into one register and a
+// transposing matrix store lays each row's features out together. (Lane = feature with the
+// pairs exchanged by shuffles moved half as much again through shared memory, which bounds
+// the MMA: 5300 cycles of epilogue slowed the next tile's first eight K blocks by half.)
+template <bool I8>
+__device__ __forceinline__ void emit_16(const RaggedParams& p, const CUtensorMap* tm_c, uint8_t* buf, int lane,
+                                        const float (&sb)[4], const float (&b)[4], const Chunk& ch,
+                                        const uint32_t (&r)[32]) {
+  const uint32_t smem = smem_u32(buf);
+  // Every branch is taken once, around straight runs over the 16 pairs: two epilogue warps
+  // per scheduler leave the latencies to be hidden by the pairs' independence.
+  float2 v[16];  // v[4 c + k]: rows 8 c + 2 (lane % 4), + 1; features 8 k + lane / 4
+  if (p.kb_total == 0) {  // no products: C = act(bias)
 #pragma unroll
-  for (int q = 0; q < 8; ++q) t[q] = __ldcg(s4 + ((col0 >> 2) + q) * 128 + r_local);
+    for (int i = 0; i < 16; ++i) v[i] = make_float2(0.0f, 0.0f);
+  } else if constexpr (I8) {
+    float2 sa[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int rr = 8 * c + 2 * (lane & 3);
+      sa[c].x = rr < ch.nrow ? __ldg(p.sa + ch.row0 + rr) : 0.0f;
+      sa[c].y = rr + 1 < ch.nrow ? __ldg(p.sa + ch.row0 + rr + 1) : 0.0f;
+    }
+    // int32 -> FP32 rounds sums of 2^24 and more to nearest (relative error 2^-24).
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int c = i >> 2, k = i & 3, at = 16 * (k >> 1) + 4 * c + 2 * (k & 1);
+      v[i] = __fmul2_rn(make_float2(static_cast<float>(static_cast<int>(r[at])), static_cast<float>(static_cast<int>(r[at + 1]))),
+                        __fmul2_rn(sa[c], make_float2(sb[k], sb[k])));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int c = i >> 2, k = i & 3, at = 16 * (k >> 1) + 4 * c + 2 * (k & 1);
+      v[i] = make_float2(__uint_as_float(r[at]), __uint_as_float(r[at + 1]));
+    }
+  }
+  if (p.bias != nullptr) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __fadd2_rn(v[i], make_float2(b[i & 3], b[i & 3]));
+  }
+  if (p.act == 1) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = act_apply2(v[i], 1);
+  } else if (p.act == 2) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = act_apply2(v[i], 2);
+  }
+  uint32_t w[16];
+  if (p.c_dtype == 1) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const __nv_bfloat162 t = __floats2bfloat162_rn(v[i].x, v[i].y);
+      w[i] = *reinterpret_cast<const uint32_t*>(&t);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const __half2 t = __floats2half2_rn(v[i].x, v[i].y);
+      w[i] = *reinterpret_cast<const uint32_t*>(&t);
+    }
+  }
+  if (lane == 0) bulk_wait_group_read<0>();  // the buffer may still be read by the last tile store
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    // Row j of 64 bytes, 16-byte unit u at u ^ ((j >> 1) & 3): the store map's 64-byte swizzle.
+    const int j = 8 * c + (lane & 7);
+    stmatrix_x4_trans(smem + j * 64 + 16 * ((lane >> 3) ^ ((j >> 1) & 3)), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+  }
+  // Whole 32-row chunks leave as a TMA tile store (clipped to C's columns), so the warp does
+  // not wait for its stores; rows past the expert's end must stay as they are, so a last
+  // chunk is stored row by row.
+  if (p.tma_store && ch.nrow == 32) {
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(tm_c, smem, ch.f0, ch.row0);
+      bulk_commit_group();
+    }
+    return;
+  }
+  __syncwarp();
+  uint16_t* C = static_cast<uint16_t*>(p.C);
+  const bool whole = ch.f0 + 32 <= p.N;
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    const int row = 8 * i + (lane >> 2), f = ch.f0 + 8 * (lane & 3);
+    const uint4 x = reinterpret_cast<const uint4*>(buf)[row * 4 + ((lane & 3) ^ ((row >> 1) & 3))];
+    if (row < ch.nrow) {
+      uint16_t* dst = C + static_cast<long long>(ch.row0 + row) * p.ldc + f;
+      if (whole) {
+        *reinterpret_cast<uint4*>(dst) = x;
+      } else {
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (f + q < p.N) dst[q] = static_cast<uint16_t>(w[q >> 1] >> (16 * (q & 1)));
+      }
+    }
+  }
+}
+
+// Partial tile of a K piece: the accumulator registers of warp quarter q and chunk c as they
+// are, 512 bytes per warp store. FP32 partials add as floats, int32 partials as integers;
+// two contributors' loads are in flight before the first add.
+__device__ __forceinline__ void slot_dump(float* slot, int q, int c, int lane, const uint32_t (&r)[32]) {
+  uint4* s4 = reinterpret_cast<uint4*>(slot) + (c * 4 + q) * 256 + lane;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s4[j * 32] = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+}
+
+__device__ __forceinline__ void slot_load(const float* slot, int q, int c, int lane, uint4 (&t)[8]) {
+  const uint4* s4 = reinterpret_cast<const uint4*>(slot) + (c * 4 + q) * 256 + lane;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) t[j] = __ldcg(s4 + j * 32);
 }
 
 template <bool I8>
-__device__ __forceinline__ void slot_add32(const uint4 (&t)[8], uint32_t (&v)[32]) {
+__device__ __forceinline__ void slot_add(const uint4 (&t)[8], uint32_t (&v)[32]) {
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    const uint32_t x[4] = {t[q].x, t[q].y, t[q].z, t[q].w};
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t x[4] = {t[j].x, t[j].y, t[j].z, t[j].w};
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
-      if constexpr (I8) v[4 * q + h] += x[h];
-      else v[4 * q + h] = __float_as_uint(__uint_as_float(v[4 * q + h]) + __uint_as_float(x[h]));
+      if constexpr (I8) v[4 * j + h] += x[h];
+      else v[4 * j + h] = __float_as_uint(__uint_as_float(v[4 * j + h]) + __uint_as_float(x[h]));
     }
   }
 }
@@ -370,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 4);
   volatile int* reduce_flag = reinterpret_cast<volatile int*>(misc + 8);
-  Plan* plan_sh = reinterpret_cast<Plan*>(misc + 16);
+  RaggedPlan* plan_sh = reinterpret_cast<RaggedPlan*>(misc + 16);
   int* bound = reinterpret_cast<int*>(misc + 32);  // [E + 1]
   int* tile0 = bound + p.E + 1;                    // [E + 1]
 
@@ -412,16 +419,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 3) {
     group_bounds(p.offsets, p.E, p.T, lane, bound);
     __syncwarp();
-    const Plan pl = make_plan(p, bound, P, lane);
-    group_tiles(bound, p.E, pl.cap, lane, tile0);
-    if (lane == 0) *plan_sh = pl;
+    const int cap = p.cap != 0 ? p.cap : choose_cap(bound, p.E, p.n_ft, P, lane);
+    const int width = group_tiles(bound, p.E, cap, lane, tile0);
+    __syncwarp();
+    if (lane == 0) {
+      const int tiles = tile0[p.E] * p.n_ft;
+      *plan_sh = RaggedPlan{cap, tiles, width, cut_along_k(tiles, width, p.kb_total, P, p.force_sched)};
+    }
   }
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // both CTAs' barriers exist before any remote arrive or copy targets them
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const Plan plan = *plan_sh;
+  const RaggedPlan plan = *plan_sh;
   const uint64_t limit = p.wait_limit_cycles;
   const bool drawn = plan.stream_k == 0 && plan.tiles > P;
   const int stage_bytes = kWBytes + plan.width * 64;
@@ -591,7 +602,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------- epilogue
     const int q = warp & 3;
     const int half = (warp - kEpiWarp0) >> 2;  // takes 32-row chunks half, half + 2, ...
-    const int r_local = q * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(q * 32) << 16;
     const int epi_tid = threadIdx.x - kEpiWarp0 * 32;
     uint8_t* buf = staging + (warp - kEpiWarp0) * kStageWarpBytes;
@@ -604,38 +614,48 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int acc = local & 1;
       const uint32_t acc_phase = (local >> 1) & 1;
       const int f0 = it.nt * 256 + static_cast<int>(rank) * 128 + q * 32;
-      // The lane's column scale and bias, loaded while the tile's MMAs run.
-      const bool live = f0 + static_cast<int>(lane) < p.N;
-      const long long col = static_cast<long long>(it.e) * p.N + f0 + lane;
-      float sb = 0.0f, b = 0.0f;
-      if (I8 && live && p.kb_total > 0) sb = __ldg(p.sb + col);
-      if (p.bias != nullptr && live) {
-        if (p.bias_dtype == 0) b = __ldg(static_cast<const float*>(p.bias) + col);
-        else if (p.bias_dtype == 1) b = __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[col]);
-        else b = __half2float(static_cast<const __half*>(p.bias)[col]);
+      // The thread's column scales and biases, loaded while the tile's MMAs run.
+      float sb[4], b[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int f = f0 + chunk_feature(p.c_dtype, static_cast<int>(lane), k);
+        const long long col = static_cast<long long>(it.e) * p.N + f;
+        sb[k] = b[k] = 0.0f;
+        if (f >= p.N || (p.c_dtype == 0 && k > 0)) continue;
+        if (I8 && p.kb_total > 0) sb[k] = __ldg(p.sb + col);
+        if (p.bias != nullptr) {
+          if (p.bias_dtype == 0) b[k] = __ldg(static_cast<const float*>(p.bias) + col);
+          else if (p.bias_dtype == 1) b[k] = __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[col]);
+          else b[k] = __half2float(static_cast<const __half*>(p.bias)[col]);
+        }
       }
       if (!__all_sync(0xffffffffu, mbar_wait(tfull_bar(acc), acc_phase, abort_flag, limit))) break;
       const int chunks = item_width(it) >> 5;
       const uint32_t tacc = tmem_base + lane_addr + acc * TN;
       const bool whole = it.kb0 == 0 && it.kb1 == p.kb_total;
+      auto load = [&](int c, uint32_t(&r)[32]) {
+        if (p.c_dtype == 0) {
+          tmem_ld_32x32b_x32_sync(tacc + c * 32, r);
+        } else {
+          tmem_ld_16x256b_x4_sync(tacc + c * 32, r);
+          tmem_ld_16x256b_x4_sync(tacc + (16u << 16) + c * 32, r + 16);
+        }
+      };
       auto emit = [&](int c, const uint32_t(&r)[32]) {
+        if (f0 >= p.N) return;
         const int n = it.nrow - 32 * c;
-        if (f0 < p.N) emit_chunk<I8>(p, &maps.c, buf, static_cast<int>(lane), sb, b, f0, it.row + 32 * c, n < 32 ? n : 32, r);
+        const Chunk ch{f0, it.row + 32 * c, n < 32 ? n : 32};
+        if (p.c_dtype == 0) emit_f32<I8>(p, &maps.c, buf, static_cast<int>(lane), sb[0], b[0], ch, r);
+        else emit_16<I8>(p, &maps.c, buf, static_cast<int>(lane), sb, b, ch, r);
       };
       float* my_slot = p.slots + ((static_cast<size_t>(cluster) * 2 + ring_slot(it)) * 2 + rank) * slot_words;
       tc_fence_after();
 #pragma unroll 1
       for (int c = half; c < chunks; c += 2) {
         uint32_t r[32];
-        tmem_ld_32x32b_x32_sync(tacc + c * 32, r);
-        if (whole) {
-          emit(c, r);
-        } else {
-          float v[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-          slot_store<32>(my_slot, r_local, c * 32, v);
-        }
+        load(c, r);
+        if (whole) emit(c, r);
+        else slot_dump(my_slot, q, c, static_cast<int>(lane), r);
       }
       tc_fence_before();
       __syncwarp();
@@ -665,10 +685,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int cc = c_lo; cc <= c_hi; cc += 2) {
               uint4 t0[8], t1[8];
-              slot_load32(slot_of(cc), r_local, c * 32, t0);
-              if (cc < c_hi) slot_load32(slot_of(cc + 1), r_local, c * 32, t1);
-              slot_add32<I8>(t0, v);
-              if (cc < c_hi) slot_add32<I8>(t1, v);
+              slot_load(slot_of(cc), q, c, static_cast<int>(lane), t0);
+              if (cc < c_hi) slot_load(slot_of(cc + 1), q, c, static_cast<int>(lane), t1);
+              slot_add<I8>(t0, v);
+              if (cc < c_hi) slot_add<I8>(t1, v);
             }
             emit(c, v);
           }

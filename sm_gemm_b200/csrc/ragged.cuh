@@ -39,9 +39,56 @@ __host__ __device__ constexpr uint32_t idesc_i8(uint32_t M, uint32_t N) {
   return (2u << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
+// 16 TMEM lanes x 32 columns as MMA fragments: register 4c + k of thread t holds lane t / 4
+// (+ 8 for k >= 2), column 8c + 2 (t % 4) + (k & 1); followed by its wait.
+__device__ __forceinline__ void tmem_ld_16x256b_x4_sync(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Four 8 x 8 matrices of 16-bit elements, each stored transposed: thread t holds row t / 4,
+// columns 2 (t % 4), + 1 of each; lane l's address takes column l % 8 of matrix l / 8.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
+}
+
+// What the CTAs of a launch agree on, computed by each from the offsets.
+struct RaggedPlan {
+  int cap;       // rows of a tile at most
+  int tiles;     // of all groups and features
+  int width;     // the widest tile's rows, rounded up to 32
+  int stream_k;  // tiles cut along K (a static schedule) instead of drawn one by one
+};
+
+// Tile heights to choose from: 256, 192, 128, 96, 64, 32 rows.
+__host__ __device__ __forceinline__ int next_cap(int cap) { return cap - (cap > 128 ? 64 : 32); }
+
+// Cycles per K block of the launch's waves of tiles of `width` rows (see choose_cap).
+__host__ __device__ __forceinline__ unsigned wave_cycles(int tiles, int width, int P) {
+  return static_cast<unsigned>((tiles + P - 1) / P) * static_cast<unsigned>(256 + width);
+}
+
+// Whether fewer tiles than clusters are cut along K: worth it when the time saved by the
+// idle clusters' help, t (1 - tiles / P) for tiles of t cycles, exceeds the fix-up of a cut
+// tile (partials written, arrival, read back by the last contributor, its epilogue).
+__host__ __device__ __forceinline__ int cut_along_k(int tiles, int width, int kb, int P, int force) {
+  if (force != 0) return force == 2;
+  if (tiles >= P || tiles == 0) return 0;
+  const float t = static_cast<float>(kb) * static_cast<float>(256 + width);
+  return t * static_cast<float>(P - tiles) > (6000.0f + 100.0f * static_cast<float>(width)) * static_cast<float>(P);
+}
+
 // Rows of one token tile: a group of `cnt` rows is cut into equal tiles of at most `tn`,
 // a multiple of 32.
-__device__ __forceinline__ int tile_width(int cnt, int tn) {
+__host__ __device__ __forceinline__ int tile_width(int cnt, int tn) {
   const int nt = (cnt + tn - 1) / tn;
   return nt == 0 ? 32 : ((cnt + nt - 1) / nt + 31) & ~31;
 }
@@ -71,8 +118,9 @@ __device__ __forceinline__ void group_bounds(const int* offsets, int E, int T, u
 }
 
 // First token tile of every group by one warp (after group_bounds): tile0[E] is their number.
-__device__ __forceinline__ void group_tiles(const int* bound, int E, int cap, uint32_t lane, int* tile0) {
-  int tiles = 0;
+// Returns the widest tile's rows, rounded up to 32.
+__device__ __forceinline__ int group_tiles(const int* bound, int E, int cap, uint32_t lane, int* tile0) {
+  int tiles = 0, width = 32;
   if (lane == 0) tile0[0] = 0;
   for (int base = 0; base < E; base += 32) {
     const int i = base + static_cast<int>(lane);
@@ -81,6 +129,7 @@ __device__ __forceinline__ void group_tiles(const int* bound, int E, int cap, ui
       const int cnt = bound[i + 1] - bound[i];
       const int w = tile_width(cnt, cap);
       nt = (cnt + w - 1) / w;
+      width = w > width ? w : width;
     }
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -90,6 +139,7 @@ __device__ __forceinline__ void group_tiles(const int* bound, int E, int cap, ui
     if (i < E) tile0[i + 1] = tiles + nt;
     tiles += __shfl_sync(0xffffffffu, nt, 31);
   }
+  return __reduce_max_sync(0xffffffffu, width);
 }
 
 }  // namespace smg

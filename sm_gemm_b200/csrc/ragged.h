@@ -37,9 +37,8 @@ struct RaggedParams {
   unsigned long long* ticket;    // draw_ticket's word
   uint32_t ticket_gen;
   int slot_words;           // 32-bit words of one CTA's partial tile: 128 x its most rows
-  int choose;               // estimate the tile height (else the highest)
+  int cap;                  // rows of a tile at most (0: chosen by the kernel)
   int tma_store;            // maps.c may be used
-  int force_cap;            // rows of a tile at most (0: by estimate)
   int force_sched;          // 1: whole tiles, 2: cut along K, 0: by estimate
   unsigned long long wait_limit_cycles;
 };
