@@ -1136,7 +1136,7 @@ smgemm_status ragged_impl(const RaggedArgs& a, void* workspace, size_t workspace
   }
   const int rows = ragged_tile_rows(a.T);
   const int64_t n_ft = (a.N + 255) / 256;
-  if ((std::min<int64_t>(a.E, a.T) + a.T / 32) * n_ft > 0x7FFFFFFF) return SMGEMM_ERR_INVALID_ARG;  // tile numbers are 32-bit
+  if ((std::min<int64_t>(a.E, a.T) + a.T / 32) * n_ft > 0x7FFFFFFF) return SMGEMM_ERR_INVALID_ARG;  // 32-bit tile numbers
   DevInfo d;
   if (current_device(d) != SMGEMM_OK) return SMGEMM_ERR_CUDA;
   const int P = ragged_max_clusters();
@@ -1178,6 +1178,7 @@ smgemm_status ragged_impl(const RaggedArgs& a, void* workspace, size_t workspace
   p.N = static_cast<int>(a.N);
   p.kb_total = static_cast<int>((a.K + bke - 1) / bke);
   p.n_ft = static_cast<int>(n_ft);
+  p.n_ft_inv = 1.0f / static_cast<float>(n_ft);
   p.w_mn_major = w_mn ? 1 : 0;
   p.idesc = i8 ? idesc_i8(256, 0) : idesc_f32acc(fmt, fmt, w_mn ? 1u : 0u, 0u, 256, 0);
   p.bias = a.bias;

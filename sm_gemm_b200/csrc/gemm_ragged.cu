@@ -73,10 +73,15 @@ __device__ __forceinline__ int choose_cap(const int* bound, int E, int n_ft, int
   return best;
 }
 
-// The tile with number t (whole, no slot).
-__device__ __noinline__ RingItem resolve(const RaggedParams& p, const int* bound, const int* tile0, int cap, int t) {
-  const int u = t / p.n_ft;
+// The tile with number t (whole, no slot): groups by binary search over their first token
+// tiles; inside a group raster order, eight token tiles at a time.
+__device__ __forceinline__ RingItem resolve(const RaggedParams& p, const int* bound, const uint8_t* w32, const int* tile0,
+                                            int t) {
+  int u = static_cast<int>(static_cast<float>(t) * p.n_ft_inv);  // t / n_ft, off by a few at most
+  while (u * p.n_ft > t) --u;
+  while ((u + 1) * p.n_ft <= t) ++u;
   int lo = 0, hi = p.E - 1;
+#pragma unroll 1
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (tile0[mid] <= u) lo = mid;
@@ -84,15 +89,14 @@ __device__ __noinline__ RingItem resolve(const RaggedParams& p, const int* bound
   }
   RingItem it;
   it.e = lo;
-  const int r0 = bound[lo], r1 = bound[lo + 1];
-  const int w = tile_width(r1 - r0, cap);
+  const int r0 = bound[lo], r1 = bound[lo + 1], first = tile0[lo], m_tiles = tile0[lo + 1] - first, w = 32 * w32[lo];
   it.mt = 0;
-  it.nt = t - tile0[lo] * p.n_ft;
-  if (tile0[lo + 1] - tile0[lo] > 1) {
+  it.nt = t - first * p.n_ft;
+  if (m_tiles > 1) {
     TileSched ts{};
-    ts.m_tiles = tile0[lo + 1] - tile0[lo];
+    ts.m_tiles = m_tiles;
     ts.n_tiles = p.n_ft;
-    ts.group_m = ts.m_tiles < 8 ? ts.m_tiles : 8;
+    ts.group_m = m_tiles < 8 ? m_tiles : 8;
     tile_coords(ts, it.nt, it.mt, it.nt);
   }
   it.row = r0 + it.mt * w;
@@ -258,10 +262,10 @@ __device__ __forceinline__ void emit_16(const RaggedParams& p, const CUtensorMap
   }
   if (p.act == 1) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = act_apply2(v[i], 1);
+    for (int i = 0; i < 16; ++i) v[i] = act_pair(v[i], 1);
   } else if (p.act == 2) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = act_apply2(v[i], 2);
+    for (int i = 0; i < 16; ++i) v[i] = act_pair(v[i], 2);
   }
   uint32_t w[16];
   if (p.c_dtype == 1) {
@@ -380,6 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   RaggedPlan* plan_sh = reinterpret_cast<RaggedPlan*>(misc + 16);
   int* bound = reinterpret_cast<int*>(misc + 32);  // [E + 1]
   int* tile0 = bound + p.E + 1;                    // [E + 1]
+  uint8_t* w32 = reinterpret_cast<uint8_t*>(tile0 + p.E + 1);  // [E]
 
   const uint32_t warp = warp_id(), lane = lane_id();
   const uint32_t rank = cluster_ctarank();
@@ -415,18 +420,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish_pair();
   }
   pdl_launch_dependents();
-  pdl_wait();
+  if (p.offsets != nullptr) pdl_wait();  // a dense product's table needs nothing from earlier kernels
   if (warp == 3) {
-    group_bounds(p.offsets, p.E, p.T, lane, bound);
-    __syncwarp();
-    const int cap = p.cap != 0 ? p.cap : choose_cap(bound, p.E, p.n_ft, P, lane);
-    const int width = group_tiles(bound, p.E, cap, lane, tile0);
+    int cap = p.cap;
+    if (cap == 0) {
+      group_table(p.offsets, p.E, p.T, 0, lane, bound, w32, tile0);
+      __syncwarp();
+      cap = choose_cap(bound, p.E, p.n_ft, P, lane);
+    }
+    const int width = group_table(p.offsets, p.E, p.T, cap, lane, bound, w32, tile0);
     __syncwarp();
     if (lane == 0) {
       const int tiles = tile0[p.E] * p.n_ft;
-      *plan_sh = RaggedPlan{cap, tiles, width, cut_along_k(tiles, width, p.kb_total, P, p.force_sched)};
+      *plan_sh = RaggedPlan{tiles, width, cut_along_k(tiles, width, p.kb_total, P, p.force_sched)};
     }
   }
+  if (p.offsets == nullptr) pdl_wait();
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // both CTAs' barriers exist before any remote arrive or copy targets them
@@ -435,6 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const RaggedPlan plan = *plan_sh;
   const uint64_t limit = p.wait_limit_cycles;
   const bool drawn = plan.stream_k == 0 && plan.tiles > P;
+  const int first_drawn = drawn ? static_waves(plan.tiles / P) * P : 0;
   const int stage_bytes = kWBytes + plan.width * 64;
   const int stages = min(kMaxStages, kStageSpace / stage_bytes);
   const int slot_words = p.slot_words;
@@ -456,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto static_next = [&]() {
       RingItem x{-1, 0, 0, 0, 0, 0, 0, 0};
       if (wi.next(s, seg)) {
-        x = resolve(p, bound, tile0, plan.cap, seg.tile);
+        x = resolve(p, bound, w32, tile0, seg.tile);
         x.kb0 = seg.kb0;
         x.kb1 = seg.kb1;
         x.tile |= seg.slot << 31;
@@ -468,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       wi.init(s, cluster);
       it = static_next();
     } else if (cluster < plan.tiles) {
-      it = resolve(p, bound, tile0, plan.cap, cluster);
+      it = resolve(p, bound, w32, tile0, cluster);
     }
     if (it.e < 0) {
       if (rank == 0) ring.publish(it, abort_flag, limit);
@@ -478,7 +488,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool first = true;
     while (ok) {
       unsigned ticket = 0;
-      if (rank == 0 && drawn && lane == 0) ticket = draw_ticket(p.ticket, p.ticket_gen, P, plan.tiles);
+      const bool draw = drawn && it.tile + P >= first_drawn;
+      if (rank == 0 && draw && lane == 0)
+        ticket = draw_ticket(p.ticket, p.ticket_gen, static_cast<unsigned>(first_drawn), plan.tiles, P);
       RingItem next{-1, 0, 0, 0, 0, 0, 0, 0};
       // The next tile is resolved and published (rank 0) in the middle of this one, once the
       // stages are full and the loads wait for the MMA anyway: done between two tiles it left
@@ -493,8 +505,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (plan.stream_k) {
           next = static_next();
         } else if (drawn) {
-          ticket = __shfl_sync(0xffffffffu, ticket, 0);
-          if (ticket < static_cast<unsigned>(plan.tiles)) next = resolve(p, bound, tile0, plan.cap, static_cast<int>(ticket));
+          ticket = draw ? __shfl_sync(0xffffffffu, ticket, 0) : static_cast<unsigned>(it.tile + P);
+          if (ticket < static_cast<unsigned>(plan.tiles)) next = resolve(p, bound, w32, tile0, static_cast<int>(ticket));
         }
         return ring.publish(next, abort_flag, limit);
       };
@@ -709,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 namespace {
 constexpr int kSmem = 1024 + kStageSpace + kEpiWarps * kStageWarpBytes + kRing * kRingEntryBytes + 8 * kBars + 32 +
-                      2 * (kRaggedMaxGroups + 1) * static_cast<int>(sizeof(int));
+                      2 * (kRaggedMaxGroups + 1) * static_cast<int>(sizeof(int)) + kRaggedMaxGroups;
 static_assert(kSmem <= 232448, "shared memory budget");
 
 cudaLaunchConfig_t config(int clusters, cudaStream_t stream, cudaLaunchAttribute* attr) {

@@ -243,7 +243,7 @@ __global__ void __maxnreg__(128)
   }
   pdl_wait();
   pdl_launch_dependents();  // after the wait: the bias kernel relies on what precedes this launch
-  if (warp == 3) group_bounds(p.offsets, p.E, p.T, lane, bound);
+  if (warp == 3) group_table(p.offsets, p.E, p.T, 0, lane, bound, nullptr, nullptr);
   __syncthreads();
   for (int e = threadIdx.x; e < p.E; e += kThreads) {
     int rank_e = e;
@@ -270,6 +270,7 @@ __global__ void __maxnreg__(128)
   s.P = static_cast<int>(gridDim.x >> 1);
   s.splits = max(1, s.P / s.tiles);
   const bool drawn = s.tiles > s.P;
+  const int first_drawn = drawn ? static_waves(s.tiles / s.P) * s.P : 0;
   Ring ring{ring_base, rfull_bar, rempty_bar, 0};
 
   if (warp == 0) {
@@ -299,13 +300,15 @@ __global__ void __maxnreg__(128)
     }
     while (ok) {
       unsigned ticket = 0;
-      if (rank == 0 && drawn && lane == 0) ticket = draw_ticket(p.ticket, p.ticket_gen, s.P, s.tiles);
+      const bool draw = drawn && it.tile + s.P >= first_drawn;
+      if (rank == 0 && draw && lane == 0)
+        ticket = draw_ticket(p.ticket, p.ticket_gen, static_cast<unsigned>(first_drawn), s.tiles, s.P);
       RingItem next{-1, 0, 0, 0, 0, 0, 0, 0};
       // As in gemm_ragged.cu, the next tile is published while this one's loads are under way.
       auto handover = [&]() {
         if (rank != 0) return true;
         if (drawn) {
-          ticket = __shfl_sync(0xffffffffu, ticket, 0);
+          ticket = draw ? __shfl_sync(0xffffffffu, ticket, 0) : static_cast<unsigned>(it.tile + s.P);
           if (ticket < static_cast<unsigned>(s.tiles)) next = resolve(p, s, bound, order, static_cast<int>(ticket));
         }
         return ring.publish(next, abort_flag, limit);
@@ -519,7 +522,7 @@ __global__ void __launch_bounds__(256) ragged_dbias_kernel(const uint16_t* __res
   __shared__ float part[8][64];
   if (!beside) pdl_wait();
   const int e = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // Bounds as in group_bounds: offsets clamped to [0, T] and to their running maximum.
+  // Bounds as in group_table: offsets clamped to [0, T] and to their running maximum.
   int lo = 0;
   for (int i = threadIdx.x; i <= e; i += 256) lo = max(lo, min(max(offsets[i], 0), T));
   lo = __reduce_max_sync(0xffffffffu, lo);

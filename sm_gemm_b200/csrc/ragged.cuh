@@ -2,6 +2,7 @@
 // tensor copies for a CTA of a pair and the int8 MMA.
 #pragma once
 
+#include "epilogue.cuh"
 #include "sm100.cuh"
 
 namespace smg {
@@ -62,7 +63,6 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uin
 
 // What the CTAs of a launch agree on, computed by each from the offsets.
 struct RaggedPlan {
-  int cap;       // rows of a tile at most
   int tiles;     // of all groups and features
   int width;     // the widest tile's rows, rounded up to 32
   int stream_k;  // tiles cut along K (a static schedule) instead of drawn one by one
@@ -93,53 +93,78 @@ __host__ __device__ __forceinline__ int tile_width(int cnt, int tn) {
   return nt == 0 ? 32 : ((cnt + nt - 1) / nt + 31) & ~31;
 }
 
-// Row bounds by one warp: bound[e] .. bound[e+1] are the rows of group e. Offsets are clamped
-// to [0, T] and to their running maximum, so that no offset makes two groups write one row
-// or any row outside the matrices.
-__device__ __forceinline__ void group_bounds(const int* offsets, int E, int T, uint32_t lane, int* bound) {
-  if (offsets == nullptr) {  // one group
-    if (lane < 2) bound[lane] = lane == 0 ? 0 : T;
-    return;
-  }
+// The group table by one warp, in shared memory: bound[e] .. bound[e+1] are the rows of group
+// e, w32[e] its tiles' height in units of 32 rows, tile0[e] its first token tile (tile0[E] =
+// their number). Offsets are clamped to [0, T] and to their running maximum, so that no
+// offset makes two groups write one row or any row outside the matrices. With cap == 0 only
+// the bounds are written. Returns the greatest tile height.
+__device__ __forceinline__ int group_table(const int* offsets, int E, int T, int cap, uint32_t lane, int* bound,
+                                           uint8_t* w32, int* tile0) {
   auto clamp_t = [&](int v) { return v < 0 ? 0 : (v > T ? T : v); };
-  int run = 0;
-  for (int base = 0; base <= E; base += 32) {
+  int run = offsets == nullptr ? 0 : clamp_t(offsets[0]), tiles = 0, width = 32;
+  if (lane == 0) {
+    bound[0] = run;
+    if (cap != 0) tile0[0] = 0;
+  }
+#pragma unroll 1
+  for (int base = 0; base < E; base += 32) {
     const int i = base + static_cast<int>(lane);
-    int v = i <= E ? clamp_t(offsets[i]) : 0;
+    int v = i < E ? (offsets == nullptr ? T : clamp_t(offsets[i + 1])) : 0;
     v = v > run ? v : run;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int o = __shfl_up_sync(0xffffffffu, v, d);
       if (static_cast<int>(lane) >= d && o > v) v = o;
     }
-    if (i <= E) bound[i] = v;
+    int prev = __shfl_up_sync(0xffffffffu, v, 1);
+    if (lane == 0) prev = run;
     run = __shfl_sync(0xffffffffu, v, 31);
-  }
-}
-
-// First token tile of every group by one warp (after group_bounds): tile0[E] is their number.
-// Returns the widest tile's rows, rounded up to 32.
-__device__ __forceinline__ int group_tiles(const int* bound, int E, int cap, uint32_t lane, int* tile0) {
-  int tiles = 0, width = 32;
-  if (lane == 0) tile0[0] = 0;
-  for (int base = 0; base < E; base += 32) {
-    const int i = base + static_cast<int>(lane);
-    int nt = 0;
-    if (i < E) {
-      const int cnt = bound[i + 1] - bound[i];
-      const int w = tile_width(cnt, cap);
+    if (i < E) bound[i + 1] = v;
+    if (cap == 0) continue;
+    const int cnt = v - prev;
+    int w = 32, nt = cnt > 0 ? 1 : 0;
+    if (cnt > 32) {
+      w = tile_width(cnt, cap);
       nt = (cnt + w - 1) / w;
-      width = w > width ? w : width;
     }
+    width = w > width ? w : width;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int o = __shfl_up_sync(0xffffffffu, nt, d);
       if (static_cast<int>(lane) >= d) nt += o;
     }
-    if (i < E) tile0[i + 1] = tiles + nt;
+    if (i < E) {
+      tile0[i + 1] = tiles + nt;
+      w32[i] = static_cast<uint8_t>(w >> 5);
+    }
     tiles += __shfl_sync(0xffffffffu, nt, 31);
   }
   return __reduce_max_sync(0xffffffffu, width);
+}
+
+// Activations of 16-bit outputs for a pair of values: as act_apply2, with one reciprocal for
+// both, 1 / (d0 d1) (the denominators are in [1, 2]): three special-function operations per
+// pair instead of four, which bound the epilogue. Two more roundings of 2^-24.
+__device__ __forceinline__ float2 x_sigmoid_pair(float2 x, float2 z) {
+  const float2 t = __fmul2_rn(make_float2(fabsf(z.x), fabsf(z.y)), make_float2(-1.4426950408889634f, -1.4426950408889634f));
+  const bool tiny0 = t.x < -120.0f, tiny1 = t.y < -120.0f;
+  float e0 = exp2_sfu(tiny0 ? t.x + 64.0f : t.x);
+  float e1 = exp2_sfu(tiny1 ? t.y + 64.0f : t.y);
+  if (tiny0) e0 *= 5.421010862427522e-20f;  // 2^-64
+  if (tiny1) e1 *= 5.421010862427522e-20f;
+  float2 d = __fadd2_rn(make_float2(1.0f, 1.0f), make_float2(e0, e1));
+  d = make_float2(fminf(d.x, 2.0f), fminf(d.y, 2.0f));  // a NaN (kept by x below) must not reach the pair's other row
+  const float r = rcp_sfu(d.x * d.y);
+  const float2 xe = __fmul2_rn(x, make_float2(z.x >= 0.0f ? 1.0f : e0, z.y >= 0.0f ? 1.0f : e1));
+  return __fmul2_rn(xe, __fmul2_rn(make_float2(r, r), make_float2(d.y, d.x)));
+}
+
+__device__ __forceinline__ float2 act_pair(float2 x, int act) {
+  if (act == 1) {
+    const float2 p = __ffma2_rn(make_float2(kGeluB, kGeluB), __fmul2_rn(x, x), make_float2(kGeluA, kGeluA));
+    return x_sigmoid_pair(x, __fmul2_rn(x, p));
+  }
+  return x_sigmoid_pair(x, x);
 }
 
 }  // namespace smg

@@ -22,6 +22,7 @@ struct RaggedParams {
   const int* offsets;       // device, E + 1 row offsets; nullptr: one group of rows [0, T)
   int E, T, N;
   int kb_total, n_ft;       // K blocks of 128 bytes; 256-feature tiles per expert
+  float n_ft_inv;           // 1 / n_ft
   int w_mn_major;
   uint32_t idesc;           // without its N field
   const void* bias;         // nullable, [E][N]

@@ -152,6 +152,27 @@ def test_rows_of_other_experts_do_not_leak(cuda_device):
     assert (dW[2] == 0).all() and (db[2] == 0).all()
 
 
+@pytest.mark.parametrize("act", ["none", "silu", "gelu_tanh"])
+@pytest.mark.parametrize("out", [BF, F32])
+def test_neighbouring_rows_do_not_share_nan(cuda_device, act, out):
+    """Rows are finished in pairs and tiles hold rows of the next expert: a NaN or infinite
+    row leaves the rows before and after it as they are."""
+    counts = [33, 1, 2, 5, 64, 7]
+    T, K, N = sum(counts) + 1, 64, 72
+    A, W = normal(115, 0, (T, K), BF), normal(115, 1, (len(counts), K, N), BF, 0.1)
+    off = offsets_of(counts)
+    bad = torch.zeros(T, dtype=torch.bool)
+    bad[[1, 12, 33, 36, 41, 43, 90, 104, T - 1]] = True
+    A[bad] = float("nan")
+    A[12] = float("inf")
+    got = sg.gemm_bf16_ragged(A.cuda(), W.cuda(), off.cuda(), act=act, out_dtype=out).cpu()
+    assert sg.check() == sg.OK
+    ref, slack, mine = _forward64(A, W, off, act=act)
+    ok = mine & ~bad
+    check_as(out, got[ok], ref[ok], slack[ok], act)
+    assert not got[mine & bad].isfinite().all(dim=1).any()
+
+
 @pytest.mark.parametrize("groups", list(GROUPS))
 @pytest.mark.parametrize("dtype,out,K,N", [(BF, BF, 136, 264), (HF, F32, 300, 200), (HF, HF, 257, 1), (BF, F32, 64, 515)])
 def test_weight_and_bias_gradients(cuda_device, groups, dtype, out, K, N):
