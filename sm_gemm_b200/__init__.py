@@ -643,49 +643,62 @@ def quantize_fp8_blockwise(X, group_rows: int = 1, *, Q=None, scales=None, strea
 
 # The int8 and ragged products. Outputs and workspaces that such a call allocates belong to
 # the stream it runs on, and a call captured in a CUDA graph gets a workspace of the graph's
-# own, so that two captured graphs (or a graph and eager calls) may run side by side.
+# own, so that two captured graphs (or a graph and eager calls) may run side by side. Small
+# calls are bound by their host time, so the checks are written out, cheapest form first.
 
-def _capturing() -> bool:
-    torch = _torch()
-    return torch.cuda.is_current_stream_capturing()
+_ragged_ws_sizes: dict = {}
+_capturing = None
 
 
-def _empty_on(stream, shape, dtype, device):
-    """torch.empty, allocated for use on `stream` (None: the current one)."""
+def _empty_on(stream, ref, shape, strides, dtype):
+    """An uninitialised tensor on `ref`'s device, allocated for use on `stream` (None: the
+    current one)."""
     torch = _torch()
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty_strided(shape, strides, dtype=dtype, device=ref.device)
     if not hasattr(stream, "cuda_stream"):
         handle = int(getattr(stream, "value", stream) or 0)
-        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+        stream = torch.cuda.ExternalStream(handle, device=ref.device) if handle else torch.cuda.default_stream(ref.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty_strided(shape, strides, dtype=dtype, device=ref.device)
 
 
-def _pitched_on(stream, lead, cols, dtype, device):
-    """An uninitialised tensor [*lead, cols] whose rows start on 16-byte boundaries."""
-    unit = {_torch().float32: 4, _torch().int8: 16}.get(dtype, 8)
-    return _empty_on(stream, (*lead, -(-cols // unit) * unit), dtype, device)[..., :cols]
+def _pitched_on(stream, ref, rows, cols, dtype, lead=None):
+    """The same, [rows, cols] (or [lead, rows, cols]) with rows that start on 16-byte boundaries."""
+    unit = 16 // dtype.itemsize
+    ld = -(-cols // unit) * unit
+    if lead is None:
+        return _empty_on(stream, ref, (rows, cols), (ld, 1), dtype)
+    return _empty_on(stream, ref, (lead, rows, cols), (rows * ld, ld, 1), dtype)
 
 
-def _ragged_workspace(E, T, N, K, kind, workspace, stream, sh, device):
+def _ragged_workspace(E, T, N, K, kind, dev, ref, workspace, stream, sh):
+    """(pointer, bytes, tensor to keep) of a call's workspace."""
+    global _capturing
     if workspace is not None:
-        return workspace, _ws_bytes(workspace)
-    nbytes = int(lib().smgemm_ragged_workspace_size(E, T, N, K, kind))
+        return workspace.data_ptr(), _ws_bytes(workspace), workspace
+    # the size depends on the kind and on the widest tile, min(T, 256) rows
+    key = (dev, kind, min(T, 256) if kind != 2 else 256)
+    nbytes = _ragged_ws_sizes.get(key)
+    if nbytes is None:
+        nbytes = int(lib().smgemm_ragged_workspace_size(E, T, N, K, kind))
+        if nbytes:
+            _ragged_ws_sizes[key] = nbytes
     if nbytes == 0:
-        return None, 0
+        return None, 0, None
+    if _capturing is None:
+        _capturing = _torch().cuda.is_current_stream_capturing
     if _capturing():
-        return _empty_on(stream, (nbytes,), _torch().uint8, device), nbytes
-    if stream is None:
-        return _workspace(nbytes, device, sh)
-    key = (device.index, int(getattr(sh, "value", sh) or 0))
+        ws = _empty_on(stream, ref, (nbytes,), (1,), _torch().uint8)
+        return ws.data_ptr(), nbytes, ws
+    key = (dev, int(getattr(sh, "value", sh) or 0))
     ws = _ws_cache.get(key)
     if ws is None or ws.numel() < nbytes:
         if ws is not None:
             _ws_retired.append(ws)
-        ws = _ws_cache[key] = _empty_on(stream, (max(nbytes, 0 if ws is None else 2 * ws.numel()),), _torch().uint8,
-                                        device)
-    return ws, ws.numel()
+        size = max(nbytes, 1 << 20, 0 if ws is None else 2 * ws.numel())
+        ws = _ws_cache[key] = _empty_on(stream, ref, (size,), (1,), _torch().uint8)
+    return ws.data_ptr(), ws.numel(), ws
 
 
 def _rows_ld(t, name):
@@ -695,6 +708,8 @@ def _rows_ld(t, name):
         raise ValueError(f"{name} must be 2-D")
     rows, cols = t.shape
     s0, s1 = t.stride()
+    if rows > 1 and cols > 1 and s1 == 1 and s0 >= cols:
+        return s0
     if rows <= 1 or cols == 0:
         if cols > 1 and s1 != 1:
             raise ValueError(f"{name} must be row-major (contiguous rows)")
@@ -711,26 +726,28 @@ def _expert_layout(t, name):
     E, rows, cols = t.shape
     if E == 0 or rows == 0 or cols == 0:
         return ROW_MAJOR, -(-max(cols, 1) // 16) * 16, 0
-    s = t.stride(0)
-    if t.stride(2) == 1 and (rows <= 1 or t.stride(1) >= cols):
-        return ROW_MAJOR, (max(t.stride(1), cols) if rows > 1 else -(-cols // 16) * 16), s
-    if t.stride(1) == 1 and (cols <= 1 or t.stride(2) >= rows):
-        return COL_MAJOR, (max(t.stride(2), rows) if cols > 1 else -(-rows // 16) * 16), s
+    s, s1, s2 = t.stride()
+    if s2 == 1 and (rows <= 1 or s1 >= cols):
+        return ROW_MAJOR, (max(s1, cols) if rows > 1 else -(-cols // 16) * 16), s
+    if s1 == 1 and (cols <= 1 or s2 >= rows):
+        return COL_MAJOR, (max(s2, rows) if cols > 1 else -(-rows // 16) * 16), s
     raise ValueError(f"{name} must have a unit stride in one of its last two dimensions")
 
 
 def _check_offsets(offsets, E):
-    torch = _torch()
-    _need(offsets.dtype == torch.int32, "offsets must be int32")
-    _need(offsets.dim() == 1 and offsets.is_contiguous(), "offsets must be a contiguous vector")
+    if offsets.dtype != _torch().int32:
+        raise ValueError("offsets must be int32")
+    if offsets.dim() != 1 or not offsets.is_contiguous():
+        raise ValueError("offsets must be a contiguous vector")
     if offsets.shape[0] != E + 1:
         raise ValueError(f"offsets must have E + 1 = {E + 1} elements, not {offsets.shape[0]}")
 
 
 def _scales(t, shape, name):
-    _shape(t, shape, name)
-    _dense(t, name)
-    _need(t.dtype == _torch().float32, f"{name} must be float32")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.dtype != _torch().float32 or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous float32")
 
 
 def _expert_bias(bias, E, N):
@@ -742,9 +759,10 @@ def _expert_bias(bias, E, N):
 
 
 def _act_code(act):
-    if act not in ACTS:
+    code = ACTS.get(act)
+    if code is None:
         raise ValueError(f"unknown activation {act!r}")
-    return ACTS[act]
+    return code
 
 
 def quantize_int8_rowwise(X, *, Q=None, scales=None, stream=None):
@@ -760,16 +778,17 @@ def quantize_int8_rowwise(X, *, Q=None, scales=None, stream=None):
     ldx = _rows_ld(X, "X")
     rows, cols = X.shape
     if Q is None:
-        Q = _pitched_on(stream, (rows,), cols, torch.int8, X.device)
+        Q = _pitched_on(stream, X, rows, cols, torch.int8)
+    elif Q.shape != X.shape or Q.dtype != torch.int8:
+        raise ValueError(f"Q must be int8 of shape {(rows, cols)}")
     if scales is None:
-        scales = _empty_on(stream, (rows,), torch.float32, X.device)
-    _shape(Q, (rows, cols), "Q")
-    _need(Q.dtype == torch.int8, "Q must be int8")
-    ldq = _rows_ld(Q, "Q")
-    _scales(scales, (rows,), "scales")
-    st = lib().quantize_int8_rowwise(X.data_ptr(), _dtype_code(X.dtype), rows, cols, ldx, Q.data_ptr(), ldq,
-                                     scales.data_ptr(), _stream(stream))
-    _check(st, "quantize_int8_rowwise")
+        scales = _empty_on(stream, X, (rows,), (1,), torch.float32)
+    else:
+        _scales(scales, (rows,), "scales")
+    st = lib().quantize_int8_rowwise(X.data_ptr(), _dtype_code(X.dtype), rows, cols, ldx, Q.data_ptr(),
+                                     _rows_ld(Q, "Q"), scales.data_ptr(), _stream(stream))
+    if st != OK:
+        raise SmgemmError(st, "quantize_int8_rowwise")
     return Q, scales
 
 
@@ -785,22 +804,26 @@ def gemm_int8_scaled(Aq, sa, Bq, sb, *, bias=None, act="none", out=None, out_dty
     torch = _torch()
     lda, ldb = _rows_ld(Aq, "Aq"), _rows_ld(Bq, "Bq")
     (M, K), (N, K2) = Aq.shape, Bq.shape
-    _need(K == K2, "Aq and Bq must agree in K")
-    _need(Aq.dtype == torch.int8 and Bq.dtype == torch.int8, "Aq and Bq must be int8 codes")
+    if K != K2:
+        raise ValueError("Aq and Bq must agree in K")
+    if Aq.dtype != torch.int8 or Bq.dtype != torch.int8:
+        raise ValueError("Aq and Bq must be int8 codes")
     _scales(sa, (M,), "sa")
     _scales(sb, (N,), "sb")
+    pbias, bias_dt = None, 0
     if bias is not None:
         _vector(bias, N, "bias")
+        pbias, bias_dt = bias.data_ptr(), _dtype_code(bias.dtype)
     if out is None:
-        out = _pitched_on(stream, (M,), N, out_dtype or torch.bfloat16, Aq.device)
+        out = _pitched_on(stream, Aq, M, N, out_dtype or torch.bfloat16)
     _out_matrix(out, M, N, "out")
     sh = _stream(stream)
-    ws, wsb = _ragged_workspace(1, M, N, K, 1, workspace, stream, sh, Aq.device)
-    st = lib().gemm_int8_scaled(M, N, K, Aq.data_ptr(), lda, sa.data_ptr(), Bq.data_ptr(), ldb, sb.data_ptr(),
-                                None if bias is None else bias.data_ptr(),
-                                _dtype_code(bias.dtype) if bias is not None else 0, _act_code(act), out.data_ptr(),
-                                _dtype_code(out.dtype), _ldc(out, M, N), None if ws is None else ws.data_ptr(), wsb, sh)
-    _check(st, "gemm_int8_scaled")
+    pws, wsb, ws = _ragged_workspace(1, M, N, K, 1, dev, Aq, workspace, stream, sh)
+    st = lib().gemm_int8_scaled(M, N, K, Aq.data_ptr(), lda, sa.data_ptr(), Bq.data_ptr(), ldb, sb.data_ptr(), pbias,
+                                bias_dt, _act_code(act), out.data_ptr(), _dtype_code(out.dtype), _ldc(out, M, N), pws,
+                                wsb, sh)
+    if st != OK:
+        raise SmgemmError(st, "gemm_int8_scaled")
     return out
 
 
@@ -824,14 +847,15 @@ def gemm_bf16_ragged(A, B, offsets, *, bias=None, act="none", out=None, out_dtyp
     _check_offsets(offsets, E)
     pbias, bias_dt = _expert_bias(bias, E, N)
     if out is None:
-        out = _pitched_on(stream, (T,), N, out_dtype or A.dtype, A.device)
+        out = _pitched_on(stream, A, T, N, out_dtype or A.dtype)
     _out_matrix(out, T, N, "out")
     sh = _stream(stream)
-    ws, wsb = _ragged_workspace(E, T, N, K, 0, workspace, stream, sh, A.device)
+    pws, wsb, ws = _ragged_workspace(E, T, N, K, 0, dev, A, workspace, stream, sh)
     st = lib().gemm_bf16_ragged(E, T, N, K, offsets.data_ptr(), A.data_ptr(), _dtype_code(A.dtype), lda, B.data_ptr(),
                                 layout, ldb, stride_b, pbias, bias_dt, _act_code(act), out.data_ptr(),
-                                _dtype_code(out.dtype), _ldc(out, T, N), None if ws is None else ws.data_ptr(), wsb, sh)
-    _check(st, "gemm_bf16_ragged")
+                                _dtype_code(out.dtype), _ldc(out, T, N), pws, wsb, sh)
+    if st != OK:
+        raise SmgemmError(st, "gemm_bf16_ragged")
     return out
 
 
@@ -848,23 +872,27 @@ def gemm_int8_ragged(Aq, sa, Bq, sb, offsets, *, bias=None, act="none", out=None
     torch = _torch()
     lda = _rows_ld(Aq, "Aq")
     layout, ldb, stride_b = _expert_layout(Bq, "Bq")
-    _need(layout == ROW_MAJOR or Bq.numel() == 0, "Bq must be [E, N, K] with contiguous K")
+    if layout != ROW_MAJOR and Bq.numel() != 0:
+        raise ValueError("Bq must be [E, N, K] with contiguous K")
     (T, K), (E, N, K2) = Aq.shape, Bq.shape
-    _need(K == K2, "Aq and Bq must agree in K")
-    _need(Aq.dtype == torch.int8 and Bq.dtype == torch.int8, "Aq and Bq must be int8 codes")
+    if K != K2:
+        raise ValueError("Aq and Bq must agree in K")
+    if Aq.dtype != torch.int8 or Bq.dtype != torch.int8:
+        raise ValueError("Aq and Bq must be int8 codes")
     _scales(sa, (T,), "sa")
     _scales(sb, (E, N), "sb")
     _check_offsets(offsets, E)
     pbias, bias_dt = _expert_bias(bias, E, N)
     if out is None:
-        out = _pitched_on(stream, (T,), N, out_dtype or torch.bfloat16, Aq.device)
+        out = _pitched_on(stream, Aq, T, N, out_dtype or torch.bfloat16)
     _out_matrix(out, T, N, "out")
     sh = _stream(stream)
-    ws, wsb = _ragged_workspace(E, T, N, K, 1, workspace, stream, sh, Aq.device)
+    pws, wsb, ws = _ragged_workspace(E, T, N, K, 1, dev, Aq, workspace, stream, sh)
     st = lib().gemm_int8_ragged(E, T, N, K, offsets.data_ptr(), Aq.data_ptr(), lda, sa.data_ptr(), Bq.data_ptr(), ldb,
                                 stride_b, sb.data_ptr(), pbias, bias_dt, _act_code(act), out.data_ptr(),
-                                _dtype_code(out.dtype), _ldc(out, T, N), None if ws is None else ws.data_ptr(), wsb, sh)
-    _check(st, "gemm_int8_ragged")
+                                _dtype_code(out.dtype), _ldc(out, T, N), pws, wsb, sh)
+    if st != OK:
+        raise SmgemmError(st, "gemm_int8_ragged")
     return out
 
 
@@ -882,23 +910,26 @@ def gemm_bf16_ragged_wgrad(A, D, offsets, *, out=None, out_dtype=None, dbias=Non
     (T, K), (T2, N) = A.shape, D.shape
     if T != T2 or A.dtype != D.dtype:
         raise ValueError("A and D must agree in rows and dtype")
-    _need(offsets.dim() == 1 and offsets.shape[0] >= 1, "offsets must be a vector of E + 1 elements")
+    if offsets.dim() != 1 or offsets.shape[0] < 1:
+        raise ValueError("offsets must be a vector of E + 1 elements")
     E = offsets.shape[0] - 1
     _check_offsets(offsets, E)
     if out is None:
-        out = _pitched_on(stream, (E, K), N, out_dtype or A.dtype, A.device)
-    _shape(out, (E, K, N), "out")
+        out = _pitched_on(stream, A, K, N, out_dtype or A.dtype, E)
+    elif out.shape != (E, K, N):
+        raise ValueError(f"out must have shape {(E, K, N)}, not {tuple(out.shape)}")
     layout, ldc, stride_c = _expert_layout(out, "out")
-    _need(layout == ROW_MAJOR, "out must be row-major matrices")
+    if layout != ROW_MAJOR:
+        raise ValueError("out must be row-major matrices")
     if dbias is not None:
         _scales(dbias, (E, N), "dbias")
     sh = _stream(stream)
-    ws, wsb = _ragged_workspace(E, T, N, K, 2, workspace, stream, sh, A.device)
+    pws, wsb, ws = _ragged_workspace(E, T, N, K, 2, dev, A, workspace, stream, sh)
     st = lib().gemm_bf16_ragged_wgrad(E, T, N, K, offsets.data_ptr(), A.data_ptr(), _dtype_code(A.dtype), lda,
                                       D.data_ptr(), ldd, out.data_ptr(), _dtype_code(out.dtype), ldc, stride_c,
-                                      None if dbias is None else dbias.data_ptr(),
-                                      None if ws is None else ws.data_ptr(), wsb, sh)
-    _check(st, "gemm_bf16_ragged_wgrad")
+                                      None if dbias is None else dbias.data_ptr(), pws, wsb, sh)
+    if st != OK:
+        raise SmgemmError(st, "gemm_bf16_ragged_wgrad")
     return out
 
 

@@ -1159,9 +1159,9 @@ smgemm_status ragged_impl(const RaggedArgs& a, void* workspace, size_t workspace
     for (int i = 0; i < 3; ++i) ok = ok && encode_2d(&m.x[i], dt, a.A, a.K, a.T, a.lda * esz, bke, 64 >> i);
     if (!ok) return SMGEMM_ERR_CUDA;
   }
-  // Tile stores, as in gemm_bf16: only when a row of C is a whole number of 16-byte units.
   const char* es = knob(kKnobEpiStore);
-  if ((a.N * elem_size(a.c_dtype)) % 16 == 0 && !(es != nullptr && std::strcmp(es, "direct") == 0)) {
+  p.whole_units = (a.N * elem_size(a.c_dtype)) % 16 == 0 ? 1 : 0;
+  if (!(es != nullptr && std::strcmp(es, "direct") == 0)) {
     const bool f32 = a.c_dtype == kF32;
     const CUtensorMapDataType cdt = f32                      ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                     : a.c_dtype == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
@@ -1310,9 +1310,9 @@ smgemm_status gemm_bf16_ragged_wgrad(int E, int64_t T, int64_t N, int64_t K, con
     }
     const uint32_t fmt = bf16 ? 1u : 0u;
     WgradParams p{};
-    // Tile stores, as in gemm_bf16: only when a row of dB is a whole number of 16-byte units.
     const char* es = knob(kKnobEpiStore);
-    if ((N * elem_size(c_dtype)) % 16 == 0 && !(es != nullptr && std::strcmp(es, "direct") == 0)) {
+    p.whole_units = (N * elem_size(c_dtype)) % 16 == 0 ? 1 : 0;
+    if (!(es != nullptr && std::strcmp(es, "direct") == 0)) {
       const uint64_t sz = static_cast<uint64_t>(elem_size(c_dtype));
       const CUtensorMapDataType cdt = c_dtype == SMGEMM_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                       : c_dtype == SMGEMM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16

@@ -141,95 +141,18 @@ struct Chunk {
   int f0, row0, nrow;
 };
 
-// Feature (0..31 of the warp's) of a thread's k-th column scale and bias: with 16-bit
-// output the thread holds fragments (features t / 4 + 8 k), with FP32 one feature, its lane.
-__device__ __forceinline__ int chunk_feature(int c_dtype, int lane, int k) {
-  return c_dtype == 0 ? lane : (lane >> 2) + 8 * k;
-}
-
-// FP32 output: lane = feature, r = its 32 rows. Scale, bias, activation, then 16 rows of 128
-// bytes at a time through the warp's 2 KB buffer.
+// 32 features x 32 rows of C^T in registers -> C. r[16 h + 4 c + k] = fragment (feature 16 h +
+// 8 (k / 2) + lane / 4, row 8 c + 2 (lane % 4) + (k & 1)); sb[k], b[k]: column scale and bias
+// of feature 8 k + lane / 4. Scale, bias, activation, cast, transposition through the warp's
+// 2 KB buffer: 16-bit rows by a transposing matrix store of neighbouring rows packed into
+// one register. (Lane = feature with the pairs exchanged by shuffles moved half as much again
+// through shared memory, which bounds the MMA: its 5300 cycles slowed the next tile's first
+// eight K blocks by half.) Every branch is taken once, around straight runs over the 16
+// pairs: two epilogue warps per scheduler leave the latencies to be hidden by the pairs'
+// independence.
 template <bool I8>
-__device__ __forceinline__ void emit_f32(const RaggedParams& p, const CUtensorMap* tm_c, uint8_t* buf, int lane, float sb,
-                                         float b, const Chunk& ch, const uint32_t (&r)[32]) {
-  float v[32];
-  if (p.kb_total == 0) {  // no products: C = act(bias)
-#pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
-  } else if constexpr (I8) {
-    const float sa = lane < ch.nrow ? __ldg(p.sa + ch.row0 + lane) : 0.0f;
-    // int32 -> FP32 rounds sums of 2^24 and more to nearest (relative error 2^-24).
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      v[j] = static_cast<float>(static_cast<int>(r[j])) * (sb * __shfl_sync(0xffffffffu, sa, j));
-  } else {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-  }
-  if (p.act != 0) {
-    // Activation in double, one copy of the code (see epi_bias_act32_f64).
-#pragma unroll 1
-    for (int j = 0; j < 32; ++j) {
-      const float y = __double2float_rn(act_apply_f64(static_cast<double>(v[0]) + static_cast<double>(b), p.act));
-#pragma unroll
-      for (int k = 0; k < 31; ++k) v[k] = v[k + 1];
-      v[31] = y;
-    }
-  } else if (p.bias != nullptr) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] += b;
-  }
-  float* C = static_cast<float*>(p.C);
-  const bool whole = ch.f0 + 32 <= p.N, tma = p.tma_store && ch.nrow == 32;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if (lane == 0) bulk_wait_group_read<0>();  // the buffer may still be read by the last tile store
-    __syncwarp();
-    // 16-byte unit u of row j at u ^ (j & 7): the 128-byte swizzle of the store's map.
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      reinterpret_cast<float*>(buf)[j * 32 + (((lane >> 2) ^ (j & 7)) << 2) + (lane & 3)] = v[16 * h + j];
-    if (tma) {
-      fence_proxy_async_shared();
-      __syncwarp();
-      if (lane == 0) {
-        tma_store_2d(tm_c, smem_u32(buf), ch.f0, ch.row0 + 16 * h);
-        bulk_commit_group();
-      }
-      continue;
-    }
-    __syncwarp();
-#pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
-      const int row = 4 * i + (lane >> 3), f = ch.f0 + 4 * (lane & 7);
-      const float4 x = reinterpret_cast<const float4*>(buf)[row * 8 + ((lane & 7) ^ (row & 7))];
-      if (16 * h + row < ch.nrow) {
-        float* dst = C + static_cast<long long>(ch.row0 + 16 * h + row) * p.ldc + f;
-        if (whole) {
-          *reinterpret_cast<float4*>(dst) = x;
-        } else {
-          const float y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (f + q < p.N) dst[q] = y[q];
-        }
-      }
-    }
-  }
-}
-
-// 16-bit output: r[16 h + 4 c + k] = fragment (feature 16 h + 8 (k / 2) + lane / 4, row
-// 8 c + 2 (lane % 4) + (k & 1)), so that neighbouring rows pack into one register and a
-// transposing matrix store lays each row's features out together. (Lane = feature with the
-// pairs exchanged by shuffles moved half as much again through shared memory, which bounds
-// the MMA: 5300 cycles of epilogue slowed the next tile's first eight K blocks by half.)
-template <bool I8>
-__device__ __forceinline__ void emit_16(const RaggedParams& p, const CUtensorMap* tm_c, uint8_t* buf, int lane,
-                                        const float (&sb)[4], const float (&b)[4], const Chunk& ch,
-                                        const uint32_t (&r)[32]) {
-  const uint32_t smem = smem_u32(buf);
-  // Every branch is taken once, around straight runs over the 16 pairs: two epilogue warps
-  // per scheduler leave the latencies to be hidden by the pairs' independence.
+__device__ __forceinline__ void emit(const RaggedParams& p, const CUtensorMap* tm_c, uint8_t* buf, int lane,
+                                     const float (&sb)[4], const float (&b)[4], const Chunk& ch, const uint32_t (&r)[32]) {
   float2 v[16];  // v[4 c + k]: rows 8 c + 2 (lane % 4), + 1; features 8 k + lane / 4
   if (p.kb_total == 0) {  // no products: C = act(bias)
 #pragma unroll
@@ -260,6 +183,58 @@ __device__ __forceinline__ void emit_16(const RaggedParams& p, const CUtensorMap
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __fadd2_rn(v[i], make_float2(b[i & 3], b[i & 3]));
   }
+  const uint32_t smem = smem_u32(buf);
+  // Chunks of 32 rows inside C leave as TMA tile stores, so the warp does not wait for them.
+  // Rows past the expert's end must stay as they are, and a box that ends past N inside a
+  // 16-byte unit may write the rest of that unit: such chunks are stored row by row.
+  const bool inside = ch.f0 + 32 <= p.N;
+  const bool tma = p.tma_store && ch.nrow == 32 && (inside || p.whole_units);
+  if (p.c_dtype == 0) {
+    if (p.act != 0) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = make_float2(act_accurate(v[i].x, p.act), act_accurate(v[i].y, p.act));
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // 16 rows of 128 bytes at a time
+      if (lane == 0) bulk_wait_group_read<0>();  // the buffer may still be read by the last tile store
+      __syncwarp();
+      // Row j, 16-byte unit u at u ^ (j & 7): the store map's 128-byte swizzle.
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int j = 8 * (i >> 2) + 2 * (lane & 3), f = 8 * (i & 3) + (lane >> 2);
+        const float2 x = v[8 * h + i];
+        reinterpret_cast<float*>(buf)[j * 32 + (((f >> 2) ^ (j & 7)) << 2) + (f & 3)] = x.x;
+        reinterpret_cast<float*>(buf)[(j + 1) * 32 + (((f >> 2) ^ ((j + 1) & 7)) << 2) + (f & 3)] = x.y;
+      }
+      if (tma) {
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(tm_c, smem, ch.f0, ch.row0 + 16 * h);
+          bulk_commit_group();
+        }
+        continue;
+      }
+      __syncwarp();
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {
+        const int row = 4 * i + (lane >> 3), f = ch.f0 + 4 * (lane & 7);
+        const float4 x = reinterpret_cast<const float4*>(buf)[row * 8 + ((lane & 7) ^ (row & 7))];
+        if (16 * h + row < ch.nrow) {
+          float* dst = static_cast<float*>(p.C) + static_cast<long long>(ch.row0 + 16 * h + row) * p.ldc + f;
+          if (inside) {
+            *reinterpret_cast<float4*>(dst) = x;
+          } else {
+            const float y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (f + q < p.N) dst[q] = y[q];
+          }
+        }
+      }
+    }
+    return;
+  }
   if (p.act == 1) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = act_pair(v[i], 1);
@@ -289,10 +264,7 @@ __device__ __forceinline__ void emit_16(const RaggedParams& p, const CUtensorMap
     const int j = 8 * c + (lane & 7);
     stmatrix_x4_trans(smem + j * 64 + 16 * ((lane >> 3) ^ ((j >> 1) & 3)), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
   }
-  // Whole 32-row chunks leave as a TMA tile store (clipped to C's columns), so the warp does
-  // not wait for its stores; rows past the expert's end must stay as they are, so a last
-  // chunk is stored row by row.
-  if (p.tma_store && ch.nrow == 32) {
+  if (tma) {
     fence_proxy_async_shared();
     __syncwarp();
     if (lane == 0) {
@@ -302,21 +274,19 @@ __device__ __forceinline__ void emit_16(const RaggedParams& p, const CUtensorMap
     return;
   }
   __syncwarp();
-  uint16_t* C = static_cast<uint16_t*>(p.C);
-  const bool whole = ch.f0 + 32 <= p.N;
 #pragma unroll 1
   for (int i = 0; i < 4; ++i) {
     const int row = 8 * i + (lane >> 2), f = ch.f0 + 8 * (lane & 3);
     const uint4 x = reinterpret_cast<const uint4*>(buf)[row * 4 + ((lane & 3) ^ ((row >> 1) & 3))];
     if (row < ch.nrow) {
-      uint16_t* dst = C + static_cast<long long>(ch.row0 + row) * p.ldc + f;
-      if (whole) {
+      uint16_t* dst = static_cast<uint16_t*>(p.C) + static_cast<long long>(ch.row0 + row) * p.ldc + f;
+      if (inside) {
         *reinterpret_cast<uint4*>(dst) = x;
       } else {
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-          if (f + q < p.N) dst[q] = static_cast<uint16_t>(w[q >> 1] >> (16 * (q & 1)));
+          if (f + q < p.N) dst[q] = static_cast<uint16_t>(y[q >> 1] >> (16 * (q & 1)));
       }
     }
   }
@@ -630,10 +600,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       float sb[4], b[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int f = f0 + chunk_feature(p.c_dtype, static_cast<int>(lane), k);
+        const int f = f0 + 8 * k + static_cast<int>(lane >> 2);
         const long long col = static_cast<long long>(it.e) * p.N + f;
         sb[k] = b[k] = 0.0f;
-        if (f >= p.N || (p.c_dtype == 0 && k > 0)) continue;
+        if (f >= p.N) continue;
         if (I8 && p.kb_total > 0) sb[k] = __ldg(p.sb + col);
         if (p.bias != nullptr) {
           if (p.bias_dtype == 0) b[k] = __ldg(static_cast<const float*>(p.bias) + col);
@@ -645,28 +615,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int chunks = item_width(it) >> 5;
       const uint32_t tacc = tmem_base + lane_addr + acc * TN;
       const bool whole = it.kb0 == 0 && it.kb1 == p.kb_total;
-      auto load = [&](int c, uint32_t(&r)[32]) {
-        if (p.c_dtype == 0) {
-          tmem_ld_32x32b_x32_sync(tacc + c * 32, r);
-        } else {
-          tmem_ld_16x256b_x4_sync(tacc + c * 32, r);
-          tmem_ld_16x256b_x4_sync(tacc + (16u << 16) + c * 32, r + 16);
-        }
-      };
-      auto emit = [&](int c, const uint32_t(&r)[32]) {
+      auto finish = [&](int c, const uint32_t(&r)[32]) {
         if (f0 >= p.N) return;
         const int n = it.nrow - 32 * c;
-        const Chunk ch{f0, it.row + 32 * c, n < 32 ? n : 32};
-        if (p.c_dtype == 0) emit_f32<I8>(p, &maps.c, buf, static_cast<int>(lane), sb[0], b[0], ch, r);
-        else emit_16<I8>(p, &maps.c, buf, static_cast<int>(lane), sb, b, ch, r);
+        emit<I8>(p, &maps.c, buf, static_cast<int>(lane), sb, b, Chunk{f0, it.row + 32 * c, n < 32 ? n : 32}, r);
       };
       float* my_slot = p.slots + ((static_cast<size_t>(cluster) * 2 + ring_slot(it)) * 2 + rank) * slot_words;
       tc_fence_after();
 #pragma unroll 1
       for (int c = half; c < chunks; c += 2) {
         uint32_t r[32];
-        load(c, r);
-        if (whole) emit(c, r);
+        tmem_ld_fragments_sync(tacc + c * 32, r);
+        if (whole) finish(c, r);
         else slot_dump(my_slot, q, c, static_cast<int>(lane), r);
       }
       tc_fence_before();
@@ -702,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               slot_add<I8>(t0, v);
               if (cc < c_hi) slot_add<I8>(t1, v);
             }
-            emit(c, v);
+            finish(c, v);
           }
         }
         if (!epi.sync(abort_flag, limit)) break;  // reduce_flag has been read

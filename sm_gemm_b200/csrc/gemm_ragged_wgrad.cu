@@ -119,13 +119,14 @@ __device__ __forceinline__ void store_chunk_tma(const CUtensorMap* map, uint32_t
   }
 }
 
-// The same without tile stores (rows that are no whole number of 16-byte units): 16-byte
+// The same without tile stores, for columns up to an N inside a 16-byte unit: 16-byte
 // stores of 128 (FP32) or 64 (16-bit) consecutive bytes of a row, where a lane's own row
 // segments would fill half a 32-byte sector per store. 16-byte chunk j of a row sits at
 // j ^ (low row bits), so that neither side's accesses share a bank.
 __device__ __forceinline__ void store_chunk(const EpiArgs& e, uint8_t* buf, int lane, int row0, int col0,
                                             const float (&v)[32]) {
   const bool whole = col0 + 32 <= e.N;
+  if (lane == 0) bulk_wait_group_read<0>();
   if (e.c_dtype == 0) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {  // 16 rows at a time
@@ -438,8 +439,8 @@ __global__ void __maxnreg__(128)
       auto emit = [&](int c, const float(&v)[32]) {
         const int col = col0 + c * 32;
         if (row0 >= p.K || col >= p.N) return;
-        if (p.tma_store) store_chunk_tma(&maps.c, smem_u32(buf), turn, static_cast<int>(lane), p.c_dtype, col, row0, it.e, v);
-        else store_chunk(e, buf, static_cast<int>(lane), row0, col, v);
+        if (p.tma_store && (p.whole_units || col + 32 <= p.N)) store_chunk_tma(&maps.c, smem_u32(buf), turn, static_cast<int>(lane), p.c_dtype, col, row0, it.e, v);
+        else store_chunk(e, buf, static_cast<int>(lane), row0, col, v);  // (waits for the buffer's tile stores)
       };
       if (it.kb1 == it.kb0) {  // an expert without rows
         float v[32];

@@ -39,7 +39,8 @@ struct RaggedParams {
   uint32_t ticket_gen;
   int slot_words;           // 32-bit words of one CTA's partial tile: 128 x its most rows
   int cap;                  // rows of a tile at most (0: chosen by the kernel)
-  int tma_store;            // maps.c may be used
+  int tma_store;            // maps.c is there
+  int whole_units;          // a row of C is a whole number of 16-byte units
   int force_sched;          // 1: whole tiles, 2: cut along K, 0: by estimate
   unsigned long long wait_limit_cycles;
 };
@@ -63,7 +64,8 @@ struct WgradParams {
   uint32_t idesc;
   void* C;
   int c_dtype;
-  int tma_store;            // maps.c may be used
+  int tma_store;            // maps.c is there
+  int whole_units;          // a row of dB is a whole number of 16-byte units
   long long ldc, stride_c;  // elements between rows / experts of dB
   float* slots;             // split tiles: [clusters][2 ranks][128][256] partials
   unsigned long long* counters;  // [clusters][2]
