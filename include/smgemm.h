@@ -289,7 +289,9 @@ smgemm_status quantize_int8_rowwise(const void* X, smgemm_dtype x_dtype, int64_t
  *
  * 8-bit integer product with a scale per token and per output channel; the sum is exact
  * (int32; any codes -128..127, K <= 131071, else SMGEMM_ERR_UNSUPPORTED), then converted to
- * FP32 (nearest), scaled, and finished as in gemm_bf16.
+ * FP32 (nearest), scaled, and finished as in gemm_bf16, but with the activation of FP32
+ * outputs evaluated in FP32 (relative error below 2^-20, plus |z| 2^-22 for GeLU's negative
+ * tail) and values below 2^-126 of the activation's input flushed to zero.
  *   Aq  device int8 [M][K], K contiguous, lda >= K; Bq device int8 [N][K] (the weight
  *       transposed), ldb >= K; both pitches multiples of 16. sa: device float [M], sb: [N].
  *   bias/act/C/ldc as in gemm_bf16. workspace: smgemm_ragged_workspace_size(1, M, N, K, 1)
@@ -316,7 +318,8 @@ smgemm_status gemm_int8_scaled(int64_t M, int64_t N, int64_t K, const int8_t* Aq
  *            elements apart (stride_b*2 a multiple of 16; the matrices must not overlap).
  *            Row-major for a forward product; the same weights as column-major [N,K]^T give
  *            the input gradient dX = dY * B_e^T.
- *   bias     device, nullable, [E][N]; act, C, ldc as in gemm_bf16. K == 0 writes act(bias).
+ *   bias     device, nullable, [E][N]; act as in gemm_int8_scaled; C, ldc as in gemm_bf16.
+ *            K == 0 writes act(bias).
  *   workspace  smgemm_ragged_workspace_size(E, T, N, K, 0) bytes, 16-byte aligned, used and
  *            shared as in gemm_bf16.
  * Deterministic; a row's result depends on its expert's rows and on the tiles of the whole

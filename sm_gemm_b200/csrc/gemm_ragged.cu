@@ -190,9 +190,12 @@ __device__ __forceinline__ void emit(const RaggedParams& p, const CUtensorMap* t
   const bool inside = ch.f0 + 32 <= p.N;
   const bool tma = p.tma_store && ch.nrow == 32 && (inside || p.whole_units);
   if (p.c_dtype == 0) {
-    if (p.act != 0) {
+    if (p.act == 1) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = make_float2(act_accurate(v[i].x, p.act), act_accurate(v[i].y, p.act));
+      for (int i = 0; i < 16; ++i) v[i] = act_accurate2(v[i], 1);
+    } else if (p.act == 2) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = act_accurate2(v[i], 2);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {  // 16 rows of 128 bytes at a time
@@ -237,10 +240,10 @@ __device__ __forceinline__ void emit(const RaggedParams& p, const CUtensorMap* t
   }
   if (p.act == 1) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = act_pair(v[i], 1);
+    for (int i = 0; i < 16; ++i) v[i] = act_fast2(v[i], 1);
   } else if (p.act == 2) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = act_pair(v[i], 2);
+    for (int i = 0; i < 16; ++i) v[i] = act_fast2(v[i], 2);
   }
   uint32_t w[16];
   if (p.c_dtype == 1) {

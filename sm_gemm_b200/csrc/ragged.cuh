@@ -147,50 +147,52 @@ __device__ __forceinline__ int group_table(const int* offsets, int E, int T, int
   return __reduce_max_sync(0xffffffffu, width);
 }
 
-// Activations of 16-bit outputs for a pair of values: as act_apply2, with one reciprocal for
-// both, 1 / (d0 d1) (the denominators are in [1, 2]): three special-function operations per
-// pair instead of four, which bound the epilogue. Two more roundings of 2^-24.
-__device__ __forceinline__ float2 x_sigmoid_pair(float2 x, float2 z) {
-  const float2 t = __fmul2_rn(make_float2(fabsf(z.x), fabsf(z.y)), make_float2(-1.4426950408889634f, -1.4426950408889634f));
-  const bool tiny0 = t.x < -120.0f, tiny1 = t.y < -120.0f;
-  float e0 = exp2_sfu(tiny0 ? t.x + 64.0f : t.x);
-  float e1 = exp2_sfu(tiny1 ? t.y + 64.0f : t.y);
-  if (tiny0) e0 *= 5.421010862427522e-20f;  // 2^-64
-  if (tiny1) e1 *= 5.421010862427522e-20f;
-  float2 d = __fadd2_rn(make_float2(1.0f, 1.0f), make_float2(e0, e1));
-  d = make_float2(fminf(d.x, 2.0f), fminf(d.y, 2.0f));  // a NaN (kept by x below) must not reach the pair's other row
-  const float r = rcp_sfu(d.x * d.y);
-  const float2 xe = __fmul2_rn(x, make_float2(z.x >= 0.0f ? 1.0f : e0, z.y >= 0.0f ? 1.0f : e1));
-  return __fmul2_rn(xe, __fmul2_rn(make_float2(r, r), make_float2(d.y, d.x)));
+// Activations, two values at a time, as x / (1 + e^-z) with SiLU's z = x and GeLU's z = 2u
+// (see epilogue.cuh): nothing cancels, e^-z may overflow to infinity (the quotient is then
+// zero), and no branch or selection is needed - the epilogue is bound by its instructions
+// (743 per 32 x 32 chunk and warp with the form that keeps e^-|z| <= 1, 50 us on 2048 rows of
+// 335 x 13335 int8). ex2.approx and rcp.approx flush subnormals: results below 2^-126 |x|
+// become zero.
+__device__ __forceinline__ float exp2_ftz(float y) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
+  return r;
 }
 
-// Activation of FP32 outputs, in FP32: the exponent's product |z| log2 e is carried in two
-// terms, so the result's relative error stays below 2^-20 plus that of z itself (exact for
-// SiLU; 2^-22 relative for GeLU, i.e. |z| 2^-22 in the factor e^-|z| of its negative tail). In
-// double precision it was within an FP32 ulp, but took 40 us where the product takes 4
-// (474 rows of 40 int8 experts, 440 x 1301).
-__device__ __forceinline__ float x_sigmoid_accurate(float x, float z) {
-  const float a = fabsf(z);
-  const float hi = __fmul_rn(a, -1.4426950408889634f);
-  const float lo = __fmaf_rn(a, -1.4426950408889634f, -hi) - a * 1.925963033500011e-8f;  // log2 e = 1.4426950216.. + 1.9e-8
-  const bool tiny = hi < -120.0f;
-  float e = exp2_sfu(tiny ? hi + 64.0f : hi);
-  if (tiny) e *= 5.421010862427522e-20f;  // 2^-64
-  e = a < 200.0f ? __fmaf_rn(e, lo * 0.6931471805599453f, e) : 0.0f;
-  const float r = __frcp_rn(1.0f + e);
-  return z >= 0.0f ? x * r : (x * e) * r;
+constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = 1.925963033500011e-8f;  // log2(e) in two FP32 terms
+
+__device__ __forceinline__ float2 act_arg(float2 x, int act) {
+  if (act != 1) return x;
+  return __fmul2_rn(x, __ffma2_rn(make_float2(kGeluB, kGeluB), __fmul2_rn(x, x), make_float2(kGeluA, kGeluA)));
 }
 
-__device__ __forceinline__ float act_accurate(float x, int act) {
-  return x_sigmoid_accurate(x, act == 1 ? x * fmaf(kGeluB, x * x, kGeluA) : x);
+// For 16-bit outputs: relative error below 2^-16 (the rounding of z log2 e, |z| log2 e <= 126,
+// is the largest term).
+__device__ __forceinline__ float2 act_fast2(float2 x, int act) {
+  const float2 t = __fmul2_rn(act_arg(x, act), make_float2(-kLog2e, -kLog2e));
+  const float2 d = __fadd2_rn(make_float2(exp2_ftz(t.x), exp2_ftz(t.y)), make_float2(1.0f, 1.0f));
+  return __fmul2_rn(x, make_float2(rcp_sfu(d.x), rcp_sfu(d.y)));
 }
 
-__device__ __forceinline__ float2 act_pair(float2 x, int act) {
-  if (act == 1) {
-    const float2 p = __ffma2_rn(make_float2(kGeluB, kGeluB), __fmul2_rn(x, x), make_float2(kGeluA, kGeluA));
-    return x_sigmoid_pair(x, __fmul2_rn(x, p));
-  }
-  return x_sigmoid_pair(x, x);
+// For FP32 outputs: -z log2 e in two terms and one Newton step on the reciprocal, relative
+// error below 2^-20 plus that of e^-z from the rounding of GeLU's z (|z| 2^-22). In double
+// precision it was within an FP32 ulp, but took 40 us where the product takes 4 (474 rows of 40
+// int8 experts, 440 x 1301).
+__device__ __forceinline__ float2 act_accurate2(float2 x, int act) {
+  const float2 z = act_arg(x, act), l = make_float2(-kLog2e, -kLog2e);
+  float2 hi = __fmul2_rn(z, l);
+  const float2 lo = __ffma2_rn(z, make_float2(-kLog2eLow, -kLog2eLow), __ffma2_rn(z, l, make_float2(-hi.x, -hi.y)));
+  // A denominator beyond 2^126 has no normal reciprocal. lo is not finite then: dropped.
+  const bool big0 = !(hi.x < 126.0f), big1 = !(hi.y < 126.0f);
+  hi = make_float2(fminf(hi.x, 126.0f), fminf(hi.y, 126.0f));
+  float2 e = make_float2(exp2_ftz(hi.x), exp2_ftz(hi.y));
+  const float2 c = make_float2(big0 || !(hi.x > -126.0f) ? 0.0f : lo.x * 0.6931471805599453f,
+                               big1 || !(hi.y > -126.0f) ? 0.0f : lo.y * 0.6931471805599453f);
+  e = __ffma2_rn(e, c, e);
+  const float2 d = __fadd2_rn(e, make_float2(1.0f, 1.0f));
+  float2 r = make_float2(rcp_sfu(d.x), rcp_sfu(d.y));
+  r = __ffma2_rn(r, __ffma2_rn(make_float2(-d.x, -d.y), r, make_float2(1.0f, 1.0f)), r);
+  return __fmul2_rn(x, r);
 }
 
 }  // namespace smg
