@@ -44,33 +44,24 @@ constexpr int kThreads = 32 * kEpiWarp0 + kEpiThreads;
 constexpr int kStageWarpBytes = 2048;  // epilogue transposition buffer per warp
 constexpr int kWBytes = 128 * 128;     // one CTA's weight tile of a stage: 128 features x 128 bytes of K
 
-// Tile height for groups that may have too few tiles at the full height, by one warp: the
-// cap with the least estimated cycles, waves x K blocks x (256 + w). A block of a tile of w
-// rows takes 256 + w cycles, since shared memory (128 bytes per cycle) bounds it: 16 KB of
-// weights and 64 w bytes of rows are written and read once per CTA (the MMA itself takes 2 w).
-__device__ __forceinline__ int choose_cap(const int* bound, int E, int n_ft, int P, uint32_t lane) {
-  int best = 256;
-  unsigned best_cycles = 0xffffffffu;
+// Cost of one tile height for groups that may have too few tiles at the full height, by one
+// warp (see wave_cycles).
+constexpr int kNumCaps = 6;  // 256, 192, 128, 96, 64, 32
+__device__ __forceinline__ int cap_of(int j) { return j < 2 ? 256 - 64 * j : 192 - 32 * j; }
+
+__device__ __forceinline__ unsigned cap_cycles(const int* bound, int E, int cap, int n_ft, int P, uint32_t lane) {
+  int tiles = 0, width = 32;
 #pragma unroll 1
-  for (int cap = 256; cap >= 32; cap = next_cap(cap)) {
-    int tiles = 0, width = 32;
-#pragma unroll 1
-    for (int i = static_cast<int>(lane); i < E; i += 32) {
-      const int cnt = bound[i + 1] - bound[i];
-      if (cnt <= 0) continue;
-      const int w = tile_width(cnt, cap);
-      tiles += (cnt + w - 1) / w;
-      width = max(width, w);
-    }
-    tiles = __reduce_add_sync(0xffffffffu, tiles);
-    width = __reduce_max_sync(0xffffffffu, width);
-    const unsigned cycles = wave_cycles(tiles * n_ft, width, P);
-    if (cycles < best_cycles) {
-      best_cycles = cycles;
-      best = cap;
-    }
+  for (int i = static_cast<int>(lane); i < E; i += 32) {
+    const int cnt = bound[i + 1] - bound[i];
+    if (cnt <= 0) continue;
+    const int w = tile_width(cnt, cap);
+    tiles += (cnt + w - 1) / w;
+    width = max(width, w);
   }
-  return best;
+  tiles = __reduce_add_sync(0xffffffffu, tiles);
+  width = __reduce_max_sync(0xffffffffu, width);
+  return wave_cycles(tiles * n_ft, width, P);
 }
 
 // The tile with number t (whole, no slot): groups by binary search over their first token
@@ -355,7 +346,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 4);
   volatile int* reduce_flag = reinterpret_cast<volatile int*>(misc + 8);
   RaggedPlan* plan_sh = reinterpret_cast<RaggedPlan*>(misc + 16);
-  int* bound = reinterpret_cast<int*>(misc + 32);  // [E + 1]
+  unsigned* cap_cost = reinterpret_cast<unsigned*>(misc + 32);              // [kNumCaps]
+  int* bound = reinterpret_cast<int*>(misc + 32 + 4 * kNumCaps);  // [E + 1]
   int* tile0 = bound + p.E + 1;                    // [E + 1]
   uint8_t* w32 = reinterpret_cast<uint8_t*>(tile0 + p.E + 1);  // [E]
 
@@ -394,13 +386,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_launch_dependents();
   if (p.offsets != nullptr) pdl_wait();  // a dense product's table needs nothing from earlier kernels
-  if (warp == 3) {
-    int cap = p.cap;
-    if (cap == 0) {
-      group_table(p.offsets, p.E, p.T, 0, lane, bound, w32, tile0);
-      __syncwarp();
-      cap = choose_cap(bound, p.E, p.n_ft, P, lane);
+  int cap = p.cap;
+  if (cap == 0) {  // the tile height depends on the offsets: one warp costs each, the cheapest wins
+    if (warp == 3) group_table(p.offsets, p.E, p.T, 0, lane, bound, w32, tile0);
+    __syncthreads();
+    if (warp >= kEpiWarp0 && warp < kEpiWarp0 + kNumCaps) {
+      const unsigned c = cap_cycles(bound, p.E, cap_of(static_cast<int>(warp) - kEpiWarp0), p.n_ft, P, lane);
+      if (lane == 0) cap_cost[warp - kEpiWarp0] = c;
     }
+    __syncthreads();
+    unsigned best = cap_cost[0];
+    cap = cap_of(0);
+#pragma unroll
+    for (int j = 1; j < kNumCaps; ++j) {
+      const unsigned c = cap_cost[j];
+      if (c < best) {
+        best = c;
+        cap = cap_of(j);
+      }
+    }
+  }
+  if (warp == 3) {
     const int width = group_table(p.offsets, p.E, p.T, cap, lane, bound, w32, tile0);
     __syncwarp();
     if (lane == 0) {
@@ -423,6 +429,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int slot_words = p.slot_words;
   Ring ring{ring_base, rfull_bar, rempty_bar, 0};
 
+  // The next item of the static schedule with a split remainder (cut along K).
+  auto static_next = [&](const TileSched& s, WorkIter& wi) {
+    RingItem x{-1, 0, 0, 0, 0, 0, 0, 0};
+    Seg seg;
+    if (wi.next(s, seg)) {
+      x = resolve(p, bound, w32, tile0, seg.tile);
+      x.kb0 = seg.kb0;
+      x.kb1 = seg.kb1;
+      x.tile |= seg.slot << 31;
+    }
+    return x;
+  };
+  auto first_item = [&](TileSched& s, WorkIter& wi) {
+    if (plan.stream_k) {
+      s = make_sched(plan.tiles, p.kb_total, P, kMinKb);
+      wi.init(s, cluster);
+      return static_next(s, wi);
+    }
+    if (cluster < plan.tiles) return resolve(p, bound, w32, tile0, cluster);
+    return RingItem{-1, 0, 0, 0, 0, 0, 0, 0};
+  };
+
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
     int stage = 0;
@@ -430,35 +458,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     long long issued = 0;
     bool ok = true;
     // The cluster's first tile is known without a draw: both CTAs' producers start on it at
-    // once. Its entry for the other warps is published once its first copies are issued.
+    // once, while rank 0's warp 3 publishes its entry for the other warps.
     TileSched s{};
     WorkIter wi{};
-    Seg seg;
-    RingItem it{-1, 0, 0, 0, 0, 0, 0, 0};
-    // The next item of the static schedule with a split remainder.
-    auto static_next = [&]() {
-      RingItem x{-1, 0, 0, 0, 0, 0, 0, 0};
-      if (wi.next(s, seg)) {
-        x = resolve(p, bound, w32, tile0, seg.tile);
-        x.kb0 = seg.kb0;
-        x.kb1 = seg.kb1;
-        x.tile |= seg.slot << 31;
-      }
-      return x;
-    };
-    if (plan.stream_k) {
-      s = make_sched(plan.tiles, p.kb_total, P, kMinKb);
-      wi.init(s, cluster);
-      it = static_next();
-    } else if (cluster < plan.tiles) {
-      it = resolve(p, bound, w32, tile0, cluster);
-    }
-    if (it.e < 0) {
-      if (rank == 0) ring.publish(it, abort_flag, limit);
-      else ring.take(it, abort_flag, limit);
-      ok = false;
-    }
-    bool first = true;
+    RingItem it = first_item(s, wi);
+    if (it.e < 0) ok = false;
+    if (rank == 1 && lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(rempty_bar, 0));  // that entry is not read here
+    ring.advance();
     while (ok) {
       unsigned ticket = 0;
       const bool draw = drawn && it.tile + P >= first_drawn;
@@ -469,14 +475,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // stages are full and the loads wait for the MMA anyway: done between two tiles it left
       // the memory queue to drain (82 -> 91 us on 64 rows over 27 experts of 2048 x 4096).
       auto handover = [&]() {
-        if (first) {  // this tile's own entry; rank 1 knows the tile and only moves the ring on
-          RingItem same = it;
-          if (!(rank == 0 ? ring.publish(it, abort_flag, limit) : ring.take(same, abort_flag, limit))) return false;
-          first = false;
-        }
         if (rank != 0) return true;
         if (plan.stream_k) {
-          next = static_next();
+          next = static_next(s, wi);
         } else if (drawn) {
           ticket = draw ? __shfl_sync(0xffffffffu, ticket, 0) : static_cast<unsigned>(it.tile + P);
           if (ticket < static_cast<unsigned>(plan.tiles)) next = resolve(p, bound, w32, tile0, static_cast<int>(ticket));
@@ -583,6 +584,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     volatile int no_abort = 0;
     mbar_wait(drain_bar, 0, &no_abort, limit);
+  } else if (warp == 3) {
+    if (rank == 0) {
+      TileSched s{};
+      WorkIter wi{};
+      ring.publish(first_item(s, wi), abort_flag, limit);
+    }
+    if (plan.stream_k && lane == 0) piece_begin(p.counters + blockIdx.x, p.gen);
   } else if (warp >= kEpiWarp0) {
     // ---------------------------------------------------------------- epilogue
     const int q = warp & 3;
@@ -640,11 +648,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long t_sk = ring_tile(it) - s.dp_tiles;
         const int c_lo = sk_owner(s, t_sk * s.kb_total);
         const int c_hi = sk_owner(s, (t_sk + 1) * s.kb_total - 1);
-        __threadfence();
         if (!epi.sync(abort_flag, limit)) break;
         if (epi_tid == 0) {
+          __threadfence();                // the whole CTA's partials, ordered before by the barrier
           const int n = c_hi - c_lo + 1;  // every cluster's range is non-empty
-          *reduce_flag = counter_arrive(p.counters + t_sk * 2 + rank, p.gen, n) == n - 1;
+          *reduce_flag = piece_arrive(p.counters + t_sk * 2 + rank, p.gen, n) == n - 1;
         }
         if (!epi.sync(abort_flag, limit)) break;
         if (*reduce_flag) {
@@ -684,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 namespace {
 constexpr int kSmem = 1024 + kStageSpace + kEpiWarps * kStageWarpBytes + kRing * kRingEntryBytes + 8 * kBars + 32 +
-                      2 * (kRaggedMaxGroups + 1) * static_cast<int>(sizeof(int)) + kRaggedMaxGroups;
+                      4 * kNumCaps + 2 * (kRaggedMaxGroups + 1) * static_cast<int>(sizeof(int)) + kRaggedMaxGroups;
 static_assert(kSmem <= 232448, "shared memory budget");
 
 cudaLaunchConfig_t config(int clusters, cudaStream_t stream, cudaLaunchAttribute* attr) {

@@ -420,6 +420,8 @@ __global__ void __maxnreg__(128)
     __syncwarp();
     volatile int no_abort = 0;
     mbar_wait(drain_bar, 0, &no_abort, limit);
+  } else if (warp == 3) {
+    if (s.splits > 1 && lane == 0) piece_begin(p.counters + blockIdx.x, p.gen);
   } else if (warp >= kEpiWarp0) {
     // ---------------------------------------------------------------- epilogue
     const int q = warp & 3;
@@ -471,9 +473,11 @@ __global__ void __maxnreg__(128)
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(tempty_bar(acc), 0));
       if (n > 1) {
-        __threadfence();
         if (!epi.sync(abort_flag, limit)) break;
-        if (epi_tid == 0) *reduce_flag = counter_arrive(p.counters + it.tile * 2 + rank, p.gen, n) == n - 1;
+        if (epi_tid == 0) {
+          __threadfence();  // the whole CTA's partials, ordered before by the barrier
+          *reduce_flag = piece_arrive(p.counters + it.tile * 2 + rank, p.gen, n) == n - 1;
+        }
         if (!epi.sync(abort_flag, limit)) break;
         if (*reduce_flag) {
           __threadfence();

@@ -76,9 +76,12 @@ struct RaggedPlan {
 // Tile heights to choose from: 256, 192, 128, 96, 64, 32 rows.
 __host__ __device__ __forceinline__ int next_cap(int cap) { return cap - (cap > 128 ? 64 : 32); }
 
-// Cycles per K block of the launch's waves of tiles of `width` rows (see choose_cap).
+// Relative cost per K block of the launch's waves of tiles of `width` rows. A block hardly gets
+// cheaper with the rows: the pair's MMA of 256 features loads its weights at 128 cycles per 16
+// elements of K whatever its N (measured per block, whole GPU: 0.27 us at 32 rows, 0.30 at 128,
+// 0.34 at 256), so lower tiles pay only where they save waves.
 __host__ __device__ __forceinline__ unsigned wave_cycles(int tiles, int width, int P) {
-  return static_cast<unsigned>((tiles + P - 1) / P) * static_cast<unsigned>(256 + width);
+  return static_cast<unsigned>((tiles + P - 1) / P) * static_cast<unsigned>(832 + width);
 }
 
 // Whether fewer tiles than clusters are cut along K: worth it when the time saved by the
@@ -87,8 +90,8 @@ __host__ __device__ __forceinline__ unsigned wave_cycles(int tiles, int width, i
 __host__ __device__ __forceinline__ int cut_along_k(int tiles, int width, int kb, int P, int force) {
   if (force != 0) return force == 2;
   if (tiles >= P || tiles == 0) return 0;
-  const float t = static_cast<float>(kb) * static_cast<float>(256 + width);
-  return t * static_cast<float>(P - tiles) > (6000.0f + 100.0f * static_cast<float>(width)) * static_cast<float>(P);
+  const float t = static_cast<float>(kb) * (450.0f + 0.25f * static_cast<float>(width));
+  return t * static_cast<float>(P - tiles) > (12000.0f + 80.0f * static_cast<float>(width)) * static_cast<float>(P);
 }
 
 // Rows of one token tile: a group of `cnt` rows is cut into equal tiles of at most `tn`,

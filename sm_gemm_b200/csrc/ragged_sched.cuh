@@ -148,4 +148,22 @@ __device__ __forceinline__ unsigned draw_ticket(unsigned long long* word, uint32
   return t;
 }
 
+// Arrival counters of the pieces of cut tiles, as counter_arrive's words (generation in the
+// upper 48 bits, arrivals in the lower 16). piece_begin makes the word this call's with no
+// arrivals, if no piece has arrived yet; it runs beside the first loads, before the first
+// arrival is due, so that an arrival is a single atomic. One that comes first all the same
+// finds a word of another generation and repeats itself by compare and swap.
+__device__ __forceinline__ void piece_begin(unsigned long long* c, unsigned long long gen) {
+  const unsigned long long cur = *reinterpret_cast<volatile unsigned long long*>(c);
+  if ((cur >> 16) != gen) atomicCAS(c, cur, gen << 16);
+}
+
+__device__ __forceinline__ int piece_arrive(unsigned long long* c, unsigned long long gen, int n) {
+  const unsigned long long old = atomicAdd(c, 1ull);
+  if ((old >> 16) != gen) return counter_arrive(c, gen, n);
+  const int count = static_cast<int>(old & 0xffffull);
+  if (count == n - 1) atomicExch(c, 0ull);  // every contributor has arrived
+  return count;
+}
+
 }  // namespace smg
