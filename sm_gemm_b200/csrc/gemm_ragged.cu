@@ -22,8 +22,8 @@
 // waits for another). Which of a row's sums are split depends on the offsets alone, so
 // results are deterministic.
 //
-// Roles: warp 0 TMA producer (rank 0's also draws and publishes tiles), warp 1 MMA issuer
-// (rank-0 CTA), warp 2 TMEM allocator, warp 3 group table, warps 4-11 epilogue.
+// Roles: warp 0 TMA producer, warp 1 MMA issuer (rank-0 CTA), warp 2 TMEM allocator, warp 3
+// group table and (rank-0 CTA) scheduler, warps 4-11 epilogue.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -318,7 +318,8 @@ __device__ __forceinline__ void slot_add(const uint4 (&t)[8], uint32_t (&v)[32])
 namespace {
 constexpr int kMaxStages = 12;
 constexpr int kStageSpace = 6 * (kWBytes + 128 * 128);  // six stages of the widest tiles
-constexpr int kBars = 2 * kMaxStages + 6 + 2 * kRing;
+constexpr int kBars = 2 * kMaxStages + 7 + 2 * kRing;
+constexpr int kRingReaders = 2 * kEpiWarps + 3;  // and both CTAs' producers, rank 0's MMA issuer
 }  // namespace
 
 template <bool I8>
@@ -340,7 +341,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto tempty_bar = [&](int b) { return bar_base + 8u * (2 * kMaxStages + 2 + b); };
   const uint32_t drain_bar = bar_base + 8u * (2 * kMaxStages + 4);
   const uint32_t epi_bar = bar_base + 8u * (2 * kMaxStages + 5);
-  const uint32_t rfull_bar = epi_bar + 8u, rempty_bar = rfull_bar + 8u * kRing;
+  const uint32_t started_bar = epi_bar + 8u;
+  const uint32_t rfull_bar = started_bar + 8u, rempty_bar = rfull_bar + 8u * kRing;
   uint8_t* misc = smem_gen + kStageSpace + kEpiWarps * kStageWarpBytes + kRing * kRingEntryBytes + 8 * kBars;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 4);
@@ -367,9 +369,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(drain_bar, 1);
     mbar_init(epi_bar, kEpiWarps);
+    mbar_init(started_bar, 1);
     for (int s = 0; s < kRing; ++s) {
       mbar_init(rfull_bar + 8 * s, 1);
-      mbar_init(rempty_bar + 8 * s, ring_readers(kEpiWarps));
+      mbar_init(rempty_bar + 8 * s, kRingReaders);
     }
     *abort_flag = 0;
     fence_barrier_init();
@@ -458,33 +461,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     long long issued = 0;
     bool ok = true;
     // The cluster's first tile is known without a draw: both CTAs' producers start on it at
-    // once, while rank 0's warp 3 publishes its entry for the other warps.
-    TileSched s{};
-    WorkIter wi{};
-    RingItem it = first_item(s, wi);
+    // once, while the scheduler publishes its entry for the other warps.
+    RingItem it;
+    {
+      TileSched s{};
+      WorkIter wi{};
+      it = first_item(s, wi);
+    }
     if (it.e < 0) ok = false;
-    if (rank == 1 && lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(rempty_bar, 0));  // that entry is not read here
+    if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(rempty_bar, 0));  // that entry is not read here
     ring.advance();
     while (ok) {
-      unsigned ticket = 0;
-      const bool draw = drawn && it.tile + P >= first_drawn;
-      if (rank == 0 && draw && lane == 0)
-        ticket = draw_ticket(p.ticket, p.ticket_gen, static_cast<unsigned>(first_drawn), plan.tiles, P);
-      RingItem next{-1, 0, 0, 0, 0, 0, 0, 0};
-      // The next tile is resolved and published (rank 0) in the middle of this one, once the
-      // stages are full and the loads wait for the MMA anyway: done between two tiles it left
-      // the memory queue to drain (82 -> 91 us on 64 rows over 27 experts of 2048 x 4096).
-      auto handover = [&]() {
-        if (rank != 0) return true;
-        if (plan.stream_k) {
-          next = static_next(s, wi);
-        } else if (drawn) {
-          ticket = draw ? __shfl_sync(0xffffffffu, ticket, 0) : static_cast<unsigned>(it.tile + P);
-          if (ticket < static_cast<unsigned>(plan.tiles)) next = resolve(p, bound, w32, tile0, static_cast<int>(ticket));
-        }
-        return ring.publish(next, abort_flag, limit);
-      };
-      const int k_next = min(it.kb1 - 1, it.kb0 + stages - 1);
+      if (rank == 0 && lane == 0) mbar_arrive(started_bar);
       const int rows = item_width(it) >> 1;  // this CTA's half of the tile's rows: a multiple of 16
       const int w_row = it.nt * 256 + static_cast<int>(rank) * 128;
       const int x_row = it.row + static_cast<int>(rank) * rows;
@@ -516,16 +504,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         ++issued;
         if (++stage == stages) { stage = 0; phase ^= 1u; }
-        if (kb == k_next && !handover()) { ok = false; break; }
       }
-      if (ok && it.kb0 == it.kb1) ok = handover();  // K == 0
-      if (!ok) break;
-      if (rank == 0) {
-        it = next;
-        ok = it.e >= 0;
-      } else {
-        ok = ring.take(it, abort_flag, limit);
-      }
+      if (ok) ok = ring.take(it, abort_flag, limit);
     }
     if (*abort_flag != 0 && rank == 0 && lane == 0) {
       // Wait (bounded, independent of the abort flag) for copies still in flight.
@@ -585,12 +565,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int no_abort = 0;
     mbar_wait(drain_bar, 0, &no_abort, limit);
   } else if (warp == 3) {
+    // ---------------------------------------------------------------- scheduler
+    if (plan.stream_k && lane == 0) piece_begin(p.counters + blockIdx.x, p.gen);
     if (rank == 0) {
       TileSched s{};
       WorkIter wi{};
-      ring.publish(first_item(s, wi), abort_flag, limit);
+      const RingItem first = first_item(s, wi);
+      schedule_tiles(
+          ring, first, started_bar,
+          [&](const RingItem& it) {
+            if (plan.stream_k) return static_next(s, wi);
+            RingItem x{-1, 0, 0, 0, 0, 0, 0, 0};
+            if (drawn) {
+              unsigned t = static_cast<unsigned>(it.tile + P);
+              if (it.tile + P >= first_drawn) {
+                if (lane == 0)
+                  t = draw_ticket(p.ticket, p.ticket_gen, static_cast<unsigned>(first_drawn), plan.tiles, P);
+                t = __shfl_sync(0xffffffffu, t, 0);
+              }
+              if (t < static_cast<unsigned>(plan.tiles)) x = resolve(p, bound, w32, tile0, static_cast<int>(t));
+            }
+            return x;
+          },
+          abort_flag, limit);
     }
-    if (plan.stream_k && lane == 0) piece_begin(p.counters + blockIdx.x, p.gen);
   } else if (warp >= kEpiWarp0) {
     // ---------------------------------------------------------------- epilogue
     const int q = warp & 3;

@@ -8,13 +8,14 @@
 // of 64, both operands read as they lie (MN-major: 64 columns x 64 rows per box). Rows of
 // the last block past the expert's end belong to the next expert and must count as zeros in
 // both operands (0 * NaN is NaN): that block is loaded in boxes of 32, 16, .. 1 rows, the
-// expert's rows from where they are and the rest from rows past T, which TMA fills with
-// zeros. The extra copies are issued once per tile.
+// expert's rows from where they are and the rest, up to a multiple of the MMA's 16, from rows
+// past T, which TMA fills with zeros. Each operand has a producer warp of its own: for experts
+// of a few rows these copies, up to a dozen per tile and operand, are what a tile takes.
 //
 // A tile costs its expert's rows, so tiles are drawn one by one (ragged_sched.cuh), the
 // experts with the most rows first; with fewer tiles than clusters each is split along its
 // rows into pieces, summed in row order by the last to finish (deterministic).
-// Roles as in gemm_ragged.cu. dbias runs beside the product: its kernel is launched
+// Roles as in gemm_ragged.cu, but warp 0 loads A and warp 2 (after allocating TMEM) D. dbias runs beside the product: its kernel is launched
 // programmatically, reads D while the product's CTAs run, and ends after them.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -42,7 +43,8 @@ constexpr int kStageBytes = 2 * kOpBytes;
 
 constexpr int kStageBufs = 2;          // epilogue staging buffers per warp
 constexpr int kStageWarpBytes = kStageBufs * 2048;
-constexpr int kBars = 2 * kStages + 6 + 2 * kRing;
+constexpr int kBars = 2 * kStages + 7 + 2 * kRing;
+constexpr int kRingReaders = 2 * kEpiWarps + 5;  // and both CTAs' producers, rank 0's MMA issuer
 constexpr int kSortGroups = 256;       // experts ordered by their rows (a quadratic ranking)
 constexpr int kMinKb = 8;              // fewest row blocks of a split tile's piece
 
@@ -208,7 +210,8 @@ __global__ void __maxnreg__(128)
   auto tfull_bar = [&](int b) { return bar_base + 8u * (2 * kStages + b); };
   auto tempty_bar = [&](int b) { return bar_base + 8u * (2 * kStages + 2 + b); };
   const uint32_t drain_bar = bar_base + 8u * (2 * kStages + 4), epi_bar = bar_base + 8u * (2 * kStages + 5);
-  const uint32_t rfull_bar = epi_bar + 8u, rempty_bar = rfull_bar + 8u * kRing;
+  const uint32_t started_bar = epi_bar + 8u;
+  const uint32_t rfull_bar = started_bar + 8u, rempty_bar = rfull_bar + 8u * kRing;
   uint8_t* misc = smem_gen + kStages * kStageBytes + kEpiWarps * kStageWarpBytes + kRing * kRingEntryBytes + 8 * kBars;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 4);
@@ -231,9 +234,10 @@ __global__ void __maxnreg__(128)
     }
     mbar_init(drain_bar, 1);
     mbar_init(epi_bar, kEpiWarps);
+    mbar_init(started_bar, 1);
     for (int s = 0; s < kRing; ++s) {
       mbar_init(rfull_bar + 8 * s, 1);
-      mbar_init(rempty_bar + 8 * s, ring_readers(kEpiWarps));
+      mbar_init(rempty_bar + 8 * s, kRingReaders);
     }
     *abort_flag = 0;
     fence_barrier_init();
@@ -274,67 +278,33 @@ __global__ void __maxnreg__(128)
   const int first_drawn = drawn ? static_waves(s.tiles / s.P) * s.P : 0;
   Ring ring{ring_base, rfull_bar, rempty_bar, 0};
 
-  if (warp == 0) {
-    // ---------------------------------------------------------------- TMA producer
+  if (warp == 0 || warp == 2) {
+    // ---------------------------------------------------------------- TMA producers: A, D
+    const bool is_a = warp == 0;
+    const CUtensorMap* box_maps = is_a ? maps.a : maps.d;
     int stage = 0;
     uint32_t phase = 0;
     long long issued = 0;
     bool ok = true;
-    RingItem it{-1, 0, 0, 0, 0, 0, 0, 0};
-    if (rank == 0) {
-      // Drawn: tile `cluster`; else piece cluster % splits of tile cluster / splits.
-      const int t = cluster / s.splits, piece = cluster % s.splits;
-      if (t < s.tiles) {
-        it = resolve(p, s, bound, order, t);
-        const int n = pieces_of(s, it.kb1);
-        const long long kbn = it.kb1;
-        if (piece < n) {
-          it.kb0 = static_cast<int>(piece * kbn / n);
-          it.kb1 = static_cast<int>((piece + 1) * kbn / n);
-        } else {
-          it.e = -1;
-        }
-      }
-      ok = ring.publish(it, abort_flag, limit) && it.e >= 0;
-    } else {
-      ok = ring.take(it, abort_flag, limit);
-    }
-    while (ok) {
-      unsigned ticket = 0;
-      const bool draw = drawn && it.tile + s.P >= first_drawn;
-      if (rank == 0 && draw && lane == 0)
-        ticket = draw_ticket(p.ticket, p.ticket_gen, static_cast<unsigned>(first_drawn), s.tiles, s.P);
-      RingItem next{-1, 0, 0, 0, 0, 0, 0, 0};
-      // As in gemm_ragged.cu, the next tile is published while this one's loads are under way.
-      auto handover = [&]() {
-        if (rank != 0) return true;
-        if (drawn) {
-          ticket = draw ? __shfl_sync(0xffffffffu, ticket, 0) : static_cast<unsigned>(it.tile + s.P);
-          if (ticket < static_cast<unsigned>(s.tiles)) next = resolve(p, s, bound, order, static_cast<int>(ticket));
-        }
-        return ring.publish(next, abort_flag, limit);
-      };
-      const int k_next = min(it.kb1 - 1, it.kb0 + kStages - 1);
-      const int a_col = it.mt * 256 + static_cast<int>(rank) * 128;
-      const int d_col = it.nt * kTileN + static_cast<int>(rank) * 128;
+    RingItem it;
+    while (ok && ring.take(it, abort_flag, limit)) {
+      if (rank == 0 && is_a && lane == 0) mbar_arrive(started_bar);
+      const int col = (is_a ? it.mt : it.nt) * 256 + static_cast<int>(rank) * 128;
       for (int kb = it.kb0; kb < it.kb1; ++kb) {
         const bool w = mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, limit);
         if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
-        const uint32_t sa = smem_base + stage * kStageBytes;
+        const uint32_t dst0 = smem_base + stage * kStageBytes + (is_a ? 0 : kOpBytes);
         const uint32_t leader_full = mapa_shared(full_bar(stage), 0);
+        const int row = it.row + kb * kBK;
+        const int valid = min(it.nrow - kb * kBK, kBK), rows = (valid + 15) & ~15;
         if (elect_one()) {
-          if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2 * kStageBytes);
-          // Rows `row`.. of both operands (two 64-column boxes each) to block row r.
-          auto load = [&](int box, int r, int row) {
-            const uint32_t dst = sa + r * 128;
-            tma_load_2d_pair(dst, &maps.a[box], leader_full, a_col, row);
-            tma_load_2d_pair(dst + kBK * 128, &maps.a[box], leader_full, a_col + 64, row);
-            tma_load_2d_pair(dst + kOpBytes, &maps.d[box], leader_full, d_col, row);
-            tma_load_2d_pair(dst + kOpBytes + kBK * 128, &maps.d[box], leader_full, d_col + 64, row);
+          if (rank == 0 && is_a) mbar_arrive_expect_tx(full_bar(stage), 1024u * rows);  // both CTAs' four 64-column boxes
+          // Rows from `from` on (two 64-column boxes) to block row r.
+          auto load = [&](int box, int r, int from) {
+            tma_load_2d_pair(dst0 + r * 128, &box_maps[box], leader_full, col, from);
+            tma_load_2d_pair(dst0 + kBK * 128 + r * 128, &box_maps[box], leader_full, col + 64, from);
           };
-          const int row = it.row + kb * kBK;
-          const int valid = it.nrow - kb * kBK;
-          if (valid >= kBK) {
+          if (valid == kBK) {
             load(0, 0, row);
           } else {
             int r = 0;
@@ -345,7 +315,7 @@ __global__ void __maxnreg__(128)
                 r += n;
               }
 #pragma unroll 1
-            for (int box = kWgradBoxes - 1, n = 1; box >= 1; --box, n <<= 1)
+            for (int box = kWgradBoxes - 1, n = 1; r < rows; --box, n <<= 1)
               if (r & n) {
                 load(box, r, p.T);  // past the last row: zeros
                 r += n;
@@ -355,18 +325,9 @@ __global__ void __maxnreg__(128)
         __syncwarp();
         ++issued;
         if (++stage == kStages) { stage = 0; phase ^= 1u; }
-        if (kb == k_next && !handover()) { ok = false; break; }
-      }
-      if (ok && it.kb0 == it.kb1) ok = handover();  // an expert without rows
-      if (!ok) break;
-      if (rank == 0) {
-        it = next;
-        ok = it.e >= 0;
-      } else {
-        ok = ring.take(it, abort_flag, limit);
       }
     }
-    if (*abort_flag != 0 && rank == 0 && lane == 0) {
+    if (*abort_flag != 0 && rank == 0 && is_a && lane == 0) {
       int st = stage;
       uint32_t ph = phase;
       volatile int no_abort = 0;
@@ -384,7 +345,7 @@ __global__ void __maxnreg__(128)
     RingItem it;
     ok = ring.take(it, abort_flag, limit);
     while (ok) {
-      const int kb0 = it.kb0, kb1 = it.kb1;
+      const int kb0 = it.kb0, kb1 = it.kb1, nrow = it.nrow;
       if (kb1 == kb0) {  // an expert without rows: the epilogue writes zeros
         ok = ring.take(it, abort_flag, limit);
         continue;
@@ -400,10 +361,11 @@ __global__ void __maxnreg__(128)
         if (!__all_sync(0xffffffffu, mbar_wait(full_bar(stage), phase, abort_flag, limit))) { ok = false; break; }
         tc_fence_after();
         const uint32_t sa = smem_base + stage * kStageBytes;
+        const int steps = (min(nrow - kb * kBK, kBK) + 15) >> 4;  // of 16 rows, as many as were loaded
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kBK / 16; ++k)
-            umma_f16_pair(d_tmem, operand_desc<128, kBK>(sa, 1, k), operand_desc<128, kBK>(sa + kOpBytes, 1, k),
+            if (k < steps) umma_f16_pair(d_tmem, operand_desc<128, kBK>(sa, 1, k), operand_desc<128, kBK>(sa + kOpBytes, 1, k),
                           p.idesc, (kb > kb0 || k > 0) ? 1u : 0u);
           umma_commit_pair(empty_bar(stage), 0x3);
         }
@@ -421,7 +383,39 @@ __global__ void __maxnreg__(128)
     volatile int no_abort = 0;
     mbar_wait(drain_bar, 0, &no_abort, limit);
   } else if (warp == 3) {
+    // ---------------------------------------------------------------- scheduler
     if (s.splits > 1 && lane == 0) piece_begin(p.counters + blockIdx.x, p.gen);
+    if (rank == 0) {
+      // First tile: `cluster`, or piece cluster % splits of tile cluster / splits.
+      RingItem first{-1, 0, 0, 0, 0, 0, 0, 0};
+      const int t0 = cluster / s.splits, piece = cluster % s.splits;
+      if (t0 < s.tiles) {
+        first = resolve(p, s, bound, order, t0);
+        const int n = pieces_of(s, first.kb1);
+        const long long kbn = first.kb1;
+        if (piece < n) {
+          first.kb0 = static_cast<int>(piece * kbn / n);
+          first.kb1 = static_cast<int>((piece + 1) * kbn / n);
+        } else {
+          first.e = -1;
+        }
+      }
+      schedule_tiles(
+          ring, first, started_bar,
+          [&](const RingItem& it) {
+            RingItem x{-1, 0, 0, 0, 0, 0, 0, 0};
+            if (drawn) {
+              unsigned t = static_cast<unsigned>(it.tile + s.P);
+              if (it.tile + s.P >= first_drawn) {
+                if (lane == 0) t = draw_ticket(p.ticket, p.ticket_gen, static_cast<unsigned>(first_drawn), s.tiles, s.P);
+                t = __shfl_sync(0xffffffffu, t, 0);
+              }
+              if (t < static_cast<unsigned>(s.tiles)) x = resolve(p, s, bound, order, static_cast<int>(t));
+            }
+            return x;
+          },
+          abort_flag, limit);
+    }
   } else if (warp >= kEpiWarp0) {
     // ---------------------------------------------------------------- epilogue
     const int q = warp & 3;

@@ -6,10 +6,10 @@
 // the path from L2 serves once (all tiles drawn: 3-5% slower on eight experts of 16384 x 4096).
 // The rest, where the clusters' different loads have to even out, is drawn tile by tile from
 // a counter in the workspace: an expert's rows decide a tile's cost, and round-robin to the
-// end left SMs idle for 37% of a launch with log-normal expert sizes. The producer warp of
-// the pair's rank-0 CTA draws ticket i + 1 when it starts tile i (the atomic's latency hides
-// behind the tile's loads) and publishes the resolved tile to both CTAs through a ring of
-// entries in their shared memory; the other warps wait for entries and release them.
+// end left SMs idle for 37% of a launch with log-normal expert sizes. The rank-0 CTA's
+// scheduler warp draws tile i + 1 when the producer starts tile i, resolves it and publishes
+// it to both CTAs through a ring of entries in their shared memory; the other warps wait for
+// entries and release them.
 #pragma once
 
 #include "sm100.cuh"
@@ -59,7 +59,7 @@ struct Ring {
   __device__ __forceinline__ uint32_t slot() const { return static_cast<uint32_t>(pos) % kRing; }
   __device__ __forceinline__ uint32_t phase() const { return (static_cast<uint32_t>(pos) / kRing) & 1u; }
 
-  // Rank 0's producer warp: hands `it` to both CTAs (one elected lane writes).
+  // Rank 0's scheduler warp: hands `it` to both CTAs (one elected lane writes).
   __device__ __forceinline__ bool publish(const RingItem& it, volatile int* abort_flag, uint64_t limit) {
     const uint32_t s = slot();
     if (!__all_sync(0xffffffffu, mbar_wait(empty + 8 * s, phase() ^ 1u, abort_flag, limit))) return false;
@@ -101,9 +101,18 @@ struct Ring {
   }
 };
 
-// Arrivals per phase of an `empty` barrier: rank 0's MMA warp and both CTAs' epilogue warps,
-// and rank 1's producer.
-__host__ __device__ constexpr int ring_readers(int epi_warps) { return 2 * epi_warps + 2; }
+// The scheduler warp's loop: publishes `it`, then next(it) once the producer has started on it
+// (it arrives on `started`), and so on up to and including the stop entry.
+template <class Next>
+__device__ __forceinline__ void schedule_tiles(Ring& ring, RingItem it, uint32_t started, Next next, volatile int* abort_flag,
+                                               uint64_t limit) {
+  uint32_t phase = 0;
+  while (ring.publish(it, abort_flag, limit) && it.e >= 0) {
+    if (!__all_sync(0xffffffffu, mbar_wait(started, phase, abort_flag, limit))) break;
+    phase ^= 1u;
+    it = next(it);
+  }
+}
 
 // Barrier of a CTA's epilogue warps whose wait is bounded (a stalled pipeline may leave some
 // of them without the tile the others are on): false when it was given up.
