@@ -175,6 +175,29 @@ def test_ragged_product(cuda_device, counts, head, tail, K, N, out, act, bias):
     assert (got[:head] == 7.0).all() and (got[T - tail:] == 7.0).all()
 
 
+@pytest.mark.parametrize("rows", ["", "96"])
+@pytest.mark.parametrize("sched", ["", "sk"])
+def test_more_tiles_than_clusters(cuda_device, monkeypatch, rows, sched):
+    monkeypatch.setenv("SMGEMM_SCHED", sched)
+    monkeypatch.setenv("SMGEMM_RAGGED_ROWS", rows)
+    counts = [1, 500, 0, 33, 90, 12, 256, 3, 410, 64, 5, 128]
+    E, T, K, N = len(counts), sum(counts), 200, 3001
+    a, b = codes(217, 0, (T, K)), codes(217, 1, (E, N, K))
+    sa, sb, off = _scales(217, 2, T), _scales(217, 3, E * N).view(E, N) / K ** 0.5, offsets_of(counts)
+    args = (pitched(a.cuda()), sa.cuda(), pitched(b.cuda()), sb.cuda(), off.cuda())
+    got = sg.gemm_int8_ragged(*args, act="gelu", out_dtype=HF)
+    again = sg.gemm_int8_ragged(*args, act="gelu", out_dtype=HF)
+    dense = sg.gemm_int8_scaled(args[0], args[1], args[2][1], args[3][1], out_dtype=F32)
+    assert sg.check() == sg.OK and torch.equal(got, again)
+    got = got.cpu()
+    for e in range(E):
+        r = slice(int(off[e]), int(off[e + 1]))
+        ref, slack = _ref(a[r], sa[r], b[e], sb[e], None, "gelu")
+        check_as(HF, got[r], ref, slack, "gelu", f"expert {e}")
+    ref, slack = _ref(a, sa, b[1], sb[1], None, "none")
+    check_as(F32, dense.cpu(), ref, slack, what="dense")
+
+
 def test_quantised_expert_layer_together(cuda_device):
     """Serving an expert FFN in int8: quantise tokens, up product with SiLU, quantise its
     BF16 result, down product - against the same chain in 64 bits on the same codes and

@@ -258,6 +258,79 @@ def test_output_rows_past_32_bit_offsets(cuda_device):
     check_as(BF, got, ref, slack)
 
 
+SKEWED = [1, 700, 0, 33, 90, 12, 256, 3, 0, 410, 64, 5, 128, 31, 77, 1, 9, 200, 0, 48, 301, 16, 2, 60]
+
+
+@pytest.mark.parametrize("rows", ["", "64", "256"])
+@pytest.mark.parametrize("sched", ["", "dp", "sk"])
+@pytest.mark.parametrize("layout,dtype,out,act", [("row", BF, BF, "silu"), ("col", HF, F32, "none")])
+def test_more_tiles_than_clusters(cuda_device, monkeypatch, layout, dtype, out, act, rows, sched):
+    """Several waves of tiles of very different heights: leading waves mapped to clusters, the
+    rest drawn (the default), or a static schedule; forced tile heights."""
+    monkeypatch.setenv("SMGEMM_SCHED", sched)
+    monkeypatch.setenv("SMGEMM_RAGGED_ROWS", rows)
+    T, K, N, E = sum(SKEWED), 72, 2312, len(SKEWED)
+    A, W, off = normal(116, 0, (T, K), dtype), normal(116, 1, (E, K, N), dtype, K ** -0.5), offsets_of(SKEWED)
+    Wd = W.cuda() if layout == "row" else W.mT.contiguous().cuda().mT
+    outs = [sg.gemm_bf16_ragged(A.cuda(), Wd, off.cuda(), act=act, out_dtype=out) for _ in range(3)]
+    assert sg.check() == sg.OK
+    ref, slack, _ = _forward64(A, W, off, act=act)
+    check_as(out, outs[0].cpu(), ref, slack, act)
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+@pytest.mark.parametrize("N", [2312, 2307])
+@pytest.mark.parametrize("out", [BF, F32])
+def test_weight_gradient_with_more_tiles_than_clusters(cuda_device, out, N):
+    T, K, E = sum(SKEWED), 264, len(SKEWED)
+    A, D, off = normal(117, 0, (T, K), BF), normal(117, 1, (T, N), BF), offsets_of(SKEWED)
+    db = torch.empty(E, N, device="cuda")
+    outs = [sg.gemm_bf16_ragged_wgrad(A.cuda(), pitched(D.cuda()), off.cuda(), out_dtype=out, dbias=db) for _ in range(2)]
+    assert sg.check() == sg.OK and torch.equal(outs[0], outs[1])
+    got, db = outs[0].cpu(), db.cpu()
+    for e in range(E):
+        r = slice(int(off[e]), int(off[e + 1]))
+        ref, slack = products64(A[r].T, D[r])
+        check_as(out, got[e], ref, slack, what=f"dW[{e}]")
+        check_as(F32, db[e], D[r].double().sum(0), D[r].double().abs().sum(0) * U32 * (SKEWED[e] + 8), what=f"dbias[{e}]")
+
+
+@pytest.mark.parametrize("op", ["product", "wgrad"])
+@pytest.mark.parametrize("K,N,out", [(200, 515, BF), (96, 40, F32), (264, 328, HF)])
+def test_register_stores(cuda_device, monkeypatch, op, K, N, out):
+    """The same results without TMA tile stores (SMGEMM_EPI_STORE=direct), bit for bit."""
+    counts, head, tail = GROUPS["32-row edges"]
+    A, W, Ad, Wd, off = _case(118, "32-row edges", K, N, BF, "row")
+    D = pitched(normal(118, 5, (A.shape[0], N), BF).cuda())
+    C = [pitched(torch.full((A.shape[0], N) if op == "product" else (len(counts), K, N), 7.0, dtype=out).cuda()) for _ in range(2)]
+    for i, store in enumerate(("", "direct")):
+        monkeypatch.setenv("SMGEMM_EPI_STORE", store)
+        if op == "product":
+            sg.gemm_bf16_ragged(Ad, Wd, off.cuda(), act="silu", out=C[i])
+        else:
+            sg.gemm_bf16_ragged_wgrad(Ad, D, off.cuda(), out=C[i])
+    assert sg.check() == sg.OK
+    assert torch.equal(C[0], C[1])
+
+
+def test_stores_stay_inside_a_wider_buffer(cuda_device):
+    """Columns right of an output whose width is odd, and rows below it, stay as they are, with
+    full 32-row chunks (tile stores) up to the last column."""
+    T, K, N, E = 640, 64, 301, 2
+    A, W, off = normal(119, 0, (T, K), BF), normal(119, 1, (E, K, N), BF, 0.1), offsets_of([320, 288])
+    D = normal(119, 2, (T, N), BF)
+    for out in (BF, F32):
+        buf = torch.full((T + 8, 320), 7.0, dtype=out, device="cuda")
+        sg.gemm_bf16_ragged(A.cuda(), pitched(W.cuda()), off.cuda(), out=buf[:T, :N])
+        wbuf = torch.full((E, K + 8, 320), 7.0, dtype=out, device="cuda")
+        sg.gemm_bf16_ragged_wgrad(A.cuda(), pitched(D.cuda()), off.cuda(), out=wbuf[:, :K, :N])
+        assert sg.check() == sg.OK
+        assert (buf[:, N:] == 7.0).all() and (buf[608:] == 7.0).all()
+        assert (wbuf[:, :, N:] == 7.0).all() and (wbuf[:, K:] == 7.0).all()
+        ref, slack, mine = _forward64(A, W, off)
+        check_as(out, buf[:T, :N].cpu()[mine], ref[mine], slack[mine])
+
+
 def test_moe_layer_forward_and_backward_together(cuda_device):
     """An expert FFN layer trained for one step: up product, SiLU, down product, and from the
     output's gradient dX, both weight gradients and the down bias's gradient, against 64-bit
@@ -325,9 +398,12 @@ def test_gradients_match_differences(cuda_device):
         assert abs(want - dW[e, k, n].double()) <= 1e-3, (e, k, n)
 
 
-def test_captured_calls_replay_with_other_offsets(cuda_device):
-    """One captured forward and weight gradient, replayed with other inputs and offsets."""
-    E, T, K, N = 6, 200, 512, 264
+@pytest.mark.parametrize("width", [264, 4872])
+def test_captured_calls_replay_with_other_offsets(cuda_device, width):
+    """One captured forward and weight gradient, replayed twice in a row with other inputs and
+    offsets; at 264 columns the tiles are cut, at 4872 they are drawn from the counter that the
+    replay before must have reset."""
+    E, T, K, N = 6, 200, 512, width
     A, W = normal(111, 0, (T, K), BF).cuda(), normal(111, 1, (E, K, N), BF, 0.05).cuda()
     D = normal(111, 2, (T, N), BF).cuda()
     off = offsets_of([50, 0, 20, 30, 0, 100]).cuda()
@@ -350,9 +426,10 @@ def test_captured_calls_replay_with_other_offsets(cuda_device):
         off.copy_(offsets_of(counts))
         for t in (C, dW, db):
             t.fill_(5.0)
-        graph.replay()
-        torch.cuda.synchronize()
-        assert sg.check() == sg.OK
+        for _ in range(2):
+            graph.replay()
+            torch.cuda.synchronize()
+            assert sg.check() == sg.OK
         got = [t.clone() for t in (C, dW, db)]
         for t in (C, dW, db):
             t.fill_(5.0)
