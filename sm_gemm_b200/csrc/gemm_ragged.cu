@@ -318,8 +318,7 @@ __device__ __forceinline__ void slot_add(const uint4 (&t)[8], uint32_t (&v)[32])
 namespace {
 constexpr int kMaxStages = 12;
 constexpr int kStageSpace = 6 * (kWBytes + 128 * 128);  // six stages of the widest tiles
-constexpr int kBars = 2 * kMaxStages + 7 + 2 * kRing;
-constexpr int kRingReaders = 2 * kEpiWarps + 3;  // and both CTAs' producers, rank 0's MMA issuer
+constexpr int kBars = 2 * kMaxStages + 7 + 3 * kRing;
 }  // namespace
 
 template <bool I8>
@@ -342,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t drain_bar = bar_base + 8u * (2 * kMaxStages + 4);
   const uint32_t epi_bar = bar_base + 8u * (2 * kMaxStages + 5);
   const uint32_t started_bar = epi_bar + 8u;
-  const uint32_t rfull_bar = started_bar + 8u, rempty_bar = rfull_bar + 8u * kRing;
+  const uint32_t rfull_bar = started_bar + 8u, rempty_bar = rfull_bar + 8u * kRing, relay_bar = rempty_bar + 8u * kRing;
   uint8_t* misc = smem_gen + kStageSpace + kEpiWarps * kStageWarpBytes + kRing * kRingEntryBytes + 8 * kBars;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 4);
@@ -372,7 +371,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(started_bar, 1);
     for (int s = 0; s < kRing; ++s) {
       mbar_init(rfull_bar + 8 * s, 1);
-      mbar_init(rempty_bar + 8 * s, kRingReaders);
+      mbar_init(rempty_bar + 8 * s, kEpiWarps + (rank == 0 ? 3 : 1));  // and the producer, MMA issuer, peer
+      mbar_init(relay_bar + 8 * s, 1);
     }
     *abort_flag = 0;
     fence_barrier_init();
@@ -431,6 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int stages = min(kMaxStages, kStageSpace / stage_bytes);
   const int slot_words = p.slot_words;
   Ring ring{ring_base, rfull_bar, rempty_bar, 0};
+  auto draws_after = [&](const RingItem& it) { return drawn && it.tile + P >= first_drawn; };
 
   // The next item of the static schedule with a split remainder (cut along K).
   auto static_next = [&](const TileSched& s, WorkIter& wi) {
@@ -469,10 +470,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       it = first_item(s, wi);
     }
     if (it.e < 0) ok = false;
-    if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(rempty_bar, 0));  // that entry is not read here
+    if (lane == 0) mbar_arrive(rempty_bar);  // that entry is not read here
     ring.advance();
     while (ok) {
-      if (rank == 0 && lane == 0) mbar_arrive(started_bar);
+      if (rank == 0 && lane == 0 && draws_after(it)) mbar_arrive(started_bar);
       const int rows = item_width(it) >> 1;  // this CTA's half of the tile's rows: a multiple of 16
       const int w_row = it.nt * 256 + static_cast<int>(rank) * 128;
       const int x_row = it.row + static_cast<int>(rank) * rows;
@@ -572,13 +573,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       WorkIter wi{};
       const RingItem first = first_item(s, wi);
       schedule_tiles(
-          ring, first, started_bar,
+          ring, first, relay_bar, started_bar, draws_after,
           [&](const RingItem& it) {
             if (plan.stream_k) return static_next(s, wi);
             RingItem x{-1, 0, 0, 0, 0, 0, 0, 0};
             if (drawn) {
               unsigned t = static_cast<unsigned>(it.tile + P);
-              if (it.tile + P >= first_drawn) {
+              if (draws_after(it)) {
                 if (lane == 0)
                   t = draw_ticket(p.ticket, p.ticket_gen, static_cast<unsigned>(first_drawn), plan.tiles, P);
                 t = __shfl_sync(0xffffffffu, t, 0);
@@ -588,6 +589,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             return x;
           },
           abort_flag, limit);
+    } else {
+      relay_tiles(ring, relay_bar, abort_flag, limit);
     }
   } else if (warp >= kEpiWarp0) {
     // ---------------------------------------------------------------- epilogue
@@ -634,6 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int c = half; c < chunks; c += 2) {
         uint32_t r[32];
+        __syncwarp();  // the load is .aligned, and stores may have left the lanes apart
         tmem_ld_fragments_sync(tacc + c * 32, r);
         if (whole) finish(c, r);
         else slot_dump(my_slot, q, c, static_cast<int>(lane), r);

@@ -43,8 +43,7 @@ constexpr int kStageBytes = 2 * kOpBytes;
 
 constexpr int kStageBufs = 2;          // epilogue staging buffers per warp
 constexpr int kStageWarpBytes = kStageBufs * 2048;
-constexpr int kBars = 2 * kStages + 7 + 2 * kRing;
-constexpr int kRingReaders = 2 * kEpiWarps + 5;  // and both CTAs' producers, rank 0's MMA issuer
+constexpr int kBars = 2 * kStages + 7 + 3 * kRing;
 constexpr int kSortGroups = 256;       // experts ordered by their rows (a quadratic ranking)
 constexpr int kMinKb = 8;              // fewest row blocks of a split tile's piece
 
@@ -211,7 +210,7 @@ __global__ void __maxnreg__(128)
   auto tempty_bar = [&](int b) { return bar_base + 8u * (2 * kStages + 2 + b); };
   const uint32_t drain_bar = bar_base + 8u * (2 * kStages + 4), epi_bar = bar_base + 8u * (2 * kStages + 5);
   const uint32_t started_bar = epi_bar + 8u;
-  const uint32_t rfull_bar = started_bar + 8u, rempty_bar = rfull_bar + 8u * kRing;
+  const uint32_t rfull_bar = started_bar + 8u, rempty_bar = rfull_bar + 8u * kRing, relay_bar = rempty_bar + 8u * kRing;
   uint8_t* misc = smem_gen + kStages * kStageBytes + kEpiWarps * kStageWarpBytes + kRing * kRingEntryBytes + 8 * kBars;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 4);
@@ -237,7 +236,8 @@ __global__ void __maxnreg__(128)
     mbar_init(started_bar, 1);
     for (int s = 0; s < kRing; ++s) {
       mbar_init(rfull_bar + 8 * s, 1);
-      mbar_init(rempty_bar + 8 * s, kRingReaders);
+      mbar_init(rempty_bar + 8 * s, kEpiWarps + (rank == 0 ? 4 : 2));  // and the producers, MMA issuer, peer
+      mbar_init(relay_bar + 8 * s, 1);
     }
     *abort_flag = 0;
     fence_barrier_init();
@@ -277,6 +277,7 @@ __global__ void __maxnreg__(128)
   const bool drawn = s.tiles > s.P;
   const int first_drawn = drawn ? static_waves(s.tiles / s.P) * s.P : 0;
   Ring ring{ring_base, rfull_bar, rempty_bar, 0};
+  auto draws_after = [&](const RingItem& it) { return drawn && it.tile + s.P >= first_drawn; };
 
   if (warp == 0 || warp == 2) {
     // ---------------------------------------------------------------- TMA producers: A, D
@@ -288,7 +289,7 @@ __global__ void __maxnreg__(128)
     bool ok = true;
     RingItem it;
     while (ok && ring.take(it, abort_flag, limit)) {
-      if (rank == 0 && is_a && lane == 0) mbar_arrive(started_bar);
+      if (rank == 0 && is_a && lane == 0 && draws_after(it)) mbar_arrive(started_bar);
       const int col = (is_a ? it.mt : it.nt) * 256 + static_cast<int>(rank) * 128;
       for (int kb = it.kb0; kb < it.kb1; ++kb) {
         const bool w = mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, limit);
@@ -401,12 +402,12 @@ __global__ void __maxnreg__(128)
         }
       }
       schedule_tiles(
-          ring, first, started_bar,
+          ring, first, relay_bar, started_bar, draws_after,
           [&](const RingItem& it) {
             RingItem x{-1, 0, 0, 0, 0, 0, 0, 0};
             if (drawn) {
               unsigned t = static_cast<unsigned>(it.tile + s.P);
-              if (it.tile + s.P >= first_drawn) {
+              if (draws_after(it)) {
                 if (lane == 0) t = draw_ticket(p.ticket, p.ticket_gen, static_cast<unsigned>(first_drawn), s.tiles, s.P);
                 t = __shfl_sync(0xffffffffu, t, 0);
               }
@@ -415,6 +416,8 @@ __global__ void __maxnreg__(128)
             return x;
           },
           abort_flag, limit);
+    } else {
+      relay_tiles(ring, relay_bar, abort_flag, limit);
     }
   } else if (warp >= kEpiWarp0) {
     // ---------------------------------------------------------------- epilogue
@@ -456,6 +459,7 @@ __global__ void __maxnreg__(128)
 #pragma unroll 1
       for (int c = 0; c < kEpiCols / 32; ++c) {
         uint32_t r[32];
+        __syncwarp();  // the load is .aligned, and stores may have left the lanes apart
         tmem_ld_32x32b_x32_sync(tacc + c * 32, r);
         float v[32];
 #pragma unroll

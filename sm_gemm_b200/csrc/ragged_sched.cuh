@@ -8,8 +8,14 @@
 // a counter in the workspace: an expert's rows decide a tile's cost, and round-robin to the
 // end left SMs idle for 37% of a launch with log-normal expert sizes. The rank-0 CTA's
 // scheduler warp draws tile i + 1 when the producer starts tile i, resolves it and publishes
-// it to both CTAs through a ring of entries in their shared memory; the other warps wait for
-// entries and release them.
+// it to its CTA's warps through a ring of entries in shared memory; they wait for entries and
+// release them. The rank-1 CTA's scheduler warp reads each entry from there and publishes it
+// in its own CTA.
+//
+// The peer is told by a remote arrival and fetches the entry itself. Written into its shared
+// memory with st.async, as this was first, launches of small tiles stopped for good, one in
+// 10^3 to 10^5, with an epilogue warp of the rank-1 CTA in a TMEM load that never returned;
+// this way none of 10^6 did.
 #pragma once
 
 #include "sm100.cuh"
@@ -32,25 +38,18 @@ struct RingItem {
 __device__ __forceinline__ int ring_tile(const RingItem& it) { return it.tile & 0x7fffffff; }
 __device__ __forceinline__ int ring_slot(const RingItem& it) { return static_cast<unsigned>(it.tile) >> 31; }
 
-// Arms an mbarrier of any CTA of the cluster for `bytes` of asynchronous stores. Relaxed:
-// nothing is published with the arrival itself (see mbar_arrive_cluster_relaxed for what a
-// release at cluster scope costs).
-__device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t cluster_addr, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_addr),
-               "r"(bytes)
-               : "memory");
-}
-
-// Asynchronous 16-byte store to any CTA of the cluster, counted in bytes on its barrier.
-__device__ __forceinline__ void st_async_16(uint32_t cluster_addr, int a, int b, int c, int d, uint32_t cluster_bar) {
+// Orders this warp's later reads after another CTA's writes before its release at cluster
+// scope, for a phase that mbar_wait has found complete.
+__device__ __forceinline__ void mbar_acquire_cluster(uint32_t bar, uint32_t parity) {
   asm volatile(
-      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(cluster_addr),
-      "r"(a), "r"(b), "r"(c), "r"(d), "r"(cluster_bar)
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t}\n" ::"r"(bar),
+      "r"(parity)
       : "memory");
 }
 
-// The ring as one warp sees it. `entries`: this CTA's entries; full: this CTA's barriers (one
-// arrival and the entry's bytes); empty: the rank-0 CTA's barriers (every reading warp).
+// A CTA's ring as one of its warps sees it. full: one arrival, the scheduler warp's; empty:
+// every reading warp of the CTA, and for rank 0 the peer's scheduler warp.
 struct Ring {
   uint32_t entries, full, empty;
   int pos;
@@ -59,25 +58,24 @@ struct Ring {
   __device__ __forceinline__ uint32_t slot() const { return static_cast<uint32_t>(pos) % kRing; }
   __device__ __forceinline__ uint32_t phase() const { return (static_cast<uint32_t>(pos) / kRing) & 1u; }
 
-  // Rank 0's scheduler warp: hands `it` to both CTAs (one elected lane writes).
+  // The scheduler warp: hands `it` to its CTA's warps.
   __device__ __forceinline__ bool publish(const RingItem& it, volatile int* abort_flag, uint64_t limit) {
     const uint32_t s = slot();
     if (!__all_sync(0xffffffffu, mbar_wait(empty + 8 * s, phase() ^ 1u, abort_flag, limit))) return false;
-    if (elect_one()) {
-#pragma unroll
-      for (uint32_t r = 0; r < 2; ++r) {
-        const uint32_t bar = mapa_shared(full + 8 * s, r), dst = mapa_shared(entries + kRingEntryBytes * s, r);
-        mbar_arrive_expect_tx_cluster(bar, kRingEntryBytes);
-        st_async_16(dst, it.e, it.row, it.nrow, it.mt, bar);
-        st_async_16(dst + 16, it.nt, it.kb0, it.kb1, it.tile, bar);
-      }
+    if (lane_id() == 0) {
+      const uint32_t a = entries + kRingEntryBytes * s;
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(it.e), "r"(it.row), "r"(it.nrow), "r"(it.mt)
+                   : "memory");
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a + 16), "r"(it.nt), "r"(it.kb0), "r"(it.kb1), "r"(it.tile)
+                   : "memory");
+      mbar_arrive(full + 8 * s);
     }
     __syncwarp();
     advance();
     return true;
   }
 
-  // Every other warp: the next entry, released at once (it is copied to registers).
+  // The reading warps: the next entry, released at once (it is copied to registers).
   __device__ __forceinline__ bool take(RingItem& it, volatile int* abort_flag, uint64_t limit) {
     const uint32_t s = slot();
     if (!__all_sync(0xffffffffu, mbar_wait(full + 8 * s, phase(), abort_flag, limit))) return false;
@@ -90,28 +88,54 @@ struct Ring {
                  : "=r"(it.nt), "=r"(it.kb0), "=r"(it.kb1), "=r"(it.tile)
                  : "r"(a + 16)
                  : "memory");
-    // The arrival's address depends on the loaded words, so it follows them; relaxed, since a
-    // release at cluster scope stalled every tile by ~1.3 us.
-    uint32_t zero;
-    asm volatile("and.b32 %0, %1, 0;" : "=r"(zero) : "r"(it.mt ^ it.tile));
-    zero = __reduce_or_sync(0xffffffffu, zero);
-    if (lane_id() == 0) mbar_arrive_cluster_relaxed(mapa_shared(empty + 8 * s + zero, 0));
+    __syncwarp();
+    if (lane_id() == 0) mbar_arrive(empty + 8 * s);
     advance();
     return it.e >= 0;
   }
 };
 
-// The scheduler warp's loop: publishes `it`, then next(it) once the producer has started on it
-// (it arrives on `started`), and so on up to and including the stop entry.
-template <class Next>
-__device__ __forceinline__ void schedule_tiles(Ring& ring, RingItem it, uint32_t started, Next next, volatile int* abort_flag,
-                                               uint64_t limit) {
+// Rank 0's scheduler warp: publishes `it` here and tells the peer's scheduler warp, then
+// next(it), and so on up to and including the stop entry. Where the next tile is drawn
+// (draws(it)), once the producer has started on this one (it arrives on `started`). `relay`:
+// the ring's barriers for this, the peer's are arrived on.
+template <class Draws, class Next>
+__device__ __forceinline__ void schedule_tiles(Ring& ring, RingItem it, uint32_t relay, uint32_t started, Draws draws, Next next,
+                                               volatile int* abort_flag, uint64_t limit) {
   uint32_t phase = 0;
-  while (ring.publish(it, abort_flag, limit) && it.e >= 0) {
-    if (!__all_sync(0xffffffffu, mbar_wait(started, phase, abort_flag, limit))) break;
-    phase ^= 1u;
+  while (true) {
+    const uint32_t peer = mapa_shared(relay + 8 * ring.slot(), 1);
+    if (!ring.publish(it, abort_flag, limit)) break;
+    if (lane_id() == 0) mbar_arrive_cluster(peer);
+    if (it.e < 0) break;
+    if (draws(it)) {
+      if (!__all_sync(0xffffffffu, mbar_wait(started, phase, abort_flag, limit))) break;
+      phase ^= 1u;
+    }
     it = next(it);
   }
+}
+
+// Rank 1's scheduler warp: fetches the entries from rank 0's ring and publishes them here.
+__device__ __forceinline__ void relay_tiles(Ring& ring, uint32_t relay, volatile int* abort_flag, uint64_t limit) {
+  RingItem it;
+  do {
+    const uint32_t s = ring.slot(), bar = relay + 8 * s;
+    if (!__all_sync(0xffffffffu, mbar_wait(bar, ring.phase(), abort_flag, limit))) return;
+    mbar_acquire_cluster(bar, ring.phase());
+    const uint32_t a = mapa_shared(ring.entries + kRingEntryBytes * s, 0);
+    asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(it.e), "=r"(it.row), "=r"(it.nrow), "=r"(it.mt)
+                 : "r"(a)
+                 : "memory");
+    asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(it.nt), "=r"(it.kb0), "=r"(it.kb1), "=r"(it.tile)
+                 : "r"(a + 16)
+                 : "memory");
+    const uint32_t free_slot = mapa_shared(ring.empty + 8 * s, 0);
+    if (!ring.publish(it, abort_flag, limit)) return;
+    if (lane_id() == 0) mbar_arrive_cluster(free_slot);  // rank 0 may reuse its entry
+  } while (it.e >= 0);
 }
 
 // Barrier of a CTA's epilogue warps whose wait is bounded (a stalled pipeline may leave some

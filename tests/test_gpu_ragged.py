@@ -467,6 +467,32 @@ def test_two_graphs_and_eager_calls_side_by_side(cuda_device):
         assert torch.equal(o, w)
 
 
+@pytest.mark.parametrize("op", ["product", "wgrad"])
+def test_small_tiles_in_thousands_of_launches(cuda_device, op):
+    """Tiles of a few rows, where the hand-over of tiles between the CTAs of a pair sets the
+    pace: every launch finishes, with the same bits."""
+    counts, K, N = [(5 * i) % 7 for i in range(40)], 600, 1669
+    off, T = offsets_of(counts).cuda(), sum(counts)
+    A = pitched(normal(121, 0, (T, K), BF).cuda())
+    if op == "product":
+        W = pitched(normal(121, 1, (len(counts), K, N), BF, K ** -0.5).cuda())
+        call = lambda out: sg.gemm_bf16_ragged(A, W, off, out=out)
+        out = pitched(torch.zeros(T, N, dtype=HF, device="cuda"))
+    else:
+        D = pitched(normal(121, 1, (T, N), BF).cuda())
+        call = lambda out: sg.gemm_bf16_ragged_wgrad(A, D, off, out=out)
+        out = pitched(torch.zeros(len(counts), K, N, dtype=HF, device="cuda"))
+    want = call(torch.empty_like(out)).clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(10):
+            call(out)
+    for _ in range(300):
+        g.replay()
+    assert sg.check() == 0
+    assert torch.equal(out, want)
+
+
 def test_outputs_of_a_call_on_another_stream(cuda_device):
     """A call given a stream allocates for that stream: its output is not memory that the
     current stream's queued work still uses."""
