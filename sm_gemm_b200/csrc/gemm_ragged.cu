@@ -431,6 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int stages = min(kMaxStages, kStageSpace / stage_bytes);
   const int slot_words = p.slot_words;
   Ring ring{ring_base, rfull_bar, rempty_bar, 0};
+  const int chain = !I8 && p.c_dtype == 0 ? kChainBlocks : kNoChains;
   auto draws_after = [&](const RingItem& it) { return drawn && it.tile + P >= first_drawn; };
 
   // The next item of the static schedule with a split remainder (cut along K).
@@ -528,38 +529,42 @@ __global__ void __launch_bounds__(kThreads, 1)
     ok = ring.take(it, abort_flag, limit);
     while (ok) {
       const uint32_t idesc = p.idesc | (static_cast<uint32_t>(item_width(it) >> 3) << 17);
-      const int acc = local & 1;
-      const uint32_t acc_phase = (local >> 1) & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait(tempty_bar(acc), acc_phase ^ 1u, abort_flag, limit))) break;
-      tc_fence_after();
-      const uint32_t d_tmem = tmem_base + acc * TN;
+      const int kb1 = it.kb1;
+      int kb = it.kb0;
       bool more = true;
-      const int kb0 = it.kb0, kb1 = it.kb1;
-      if (kb0 == kb1) more = ring.take(it, abort_flag, limit);
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (kb == kb1 - 1) more = ring.take(it, abort_flag, limit);  // behind the MMAs in flight
-        if (!__all_sync(0xffffffffu, mbar_wait(full_bar(stage), phase, abort_flag, limit))) { ok = false; break; }
+      if (kb == kb1) more = ring.take(it, abort_flag, limit);  // K == 0
+      do {  // one chain of MMAs on one accumulator
+        const int acc = local & 1;
+        const uint32_t acc_phase = (local >> 1) & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(tempty_bar(acc), acc_phase ^ 1u, abort_flag, limit))) { ok = false; break; }
         tc_fence_after();
-        const uint32_t sw = smem_base + stage * stage_bytes;
-        const uint32_t sx = sw + kWBytes;
-        if (elect_one()) {
+        const uint32_t d_tmem = tmem_base + acc * TN;
+        const int first = kb, last = min(kb + chain, kb1);
+        for (; kb < last; ++kb) {
+          if (kb == kb1 - 1) more = ring.take(it, abort_flag, limit);  // behind the MMAs in flight
+          if (!__all_sync(0xffffffffu, mbar_wait(full_bar(stage), phase, abort_flag, limit))) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t sw = smem_base + stage * stage_bytes;
+          const uint32_t sx = sw + kWBytes;
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t accum = (kb > kb0 || k > 0) ? 1u : 0u;
-            const uint64_t xd = sdesc_sw128(sx + 32 * k, 16, 1024);
-            if constexpr (I8) umma_i8_pair(d_tmem, sdesc_sw128(sw + 32 * k, 16, 1024), xd, idesc, accum);
-            else umma_f16_pair(d_tmem, operand_desc<128, 64>(sw, p.w_mn_major, k), xd, idesc, accum);
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t accum = (kb > first || k > 0) ? 1u : 0u;
+              const uint64_t xd = sdesc_sw128(sx + 32 * k, 16, 1024);
+              if constexpr (I8) umma_i8_pair(d_tmem, sdesc_sw128(sw + 32 * k, 16, 1024), xd, idesc, accum);
+              else umma_f16_pair(d_tmem, operand_desc<128, 64>(sw, p.w_mn_major, k), xd, idesc, accum);
+            }
+            umma_commit_pair(empty_bar(stage), 0x3);
           }
-          umma_commit_pair(empty_bar(stage), 0x3);
+          __syncwarp();
+          if (++stage == stages) { stage = 0; phase ^= 1u; }
         }
+        if (!ok) break;
+        if (elect_one()) umma_commit_pair(tfull_bar(acc), 0x3);
         __syncwarp();
-        if (++stage == stages) { stage = 0; phase ^= 1u; }
-      }
-      if (!ok) break;
-      if (elect_one()) umma_commit_pair(tfull_bar(acc), 0x3);
-      __syncwarp();
-      ++local;
-      ok = more;
+        ++local;
+      } while (kb < kb1);
+      ok = ok && more;
     }
     if (elect_one()) umma_commit_pair(drain_bar, 0x1);
     __syncwarp();
@@ -605,8 +610,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     int local = 0;
     RingItem it;
     while (ring.take(it, abort_flag, limit)) {
-      const int acc = local & 1;
-      const uint32_t acc_phase = (local >> 1) & 1;
       const int f0 = it.nt * 256 + static_cast<int>(rank) * 128 + q * 32;
       // The thread's column scales and biases, loaded while the tile's MMAs run.
       float sb[4], b[4];
@@ -623,9 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           else b[k] = __half2float(static_cast<const __half*>(p.bias)[col]);
         }
       }
-      if (!__all_sync(0xffffffffu, mbar_wait(tfull_bar(acc), acc_phase, abort_flag, limit))) break;
       const int chunks = item_width(it) >> 5;
-      const uint32_t tacc = tmem_base + lane_addr + acc * TN;
       const bool whole = it.kb0 == 0 && it.kb1 == p.kb_total;
       auto finish = [&](int c, const uint32_t(&r)[32]) {
         if (f0 >= p.N) return;
@@ -633,18 +634,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         emit<I8>(p, &maps.c, buf, static_cast<int>(lane), sb, b, Chunk{f0, it.row + 32 * c, n < 32 ? n : 32}, r);
       };
       float* my_slot = p.slots + ((static_cast<size_t>(cluster) * 2 + ring_slot(it)) * 2 + rank) * slot_words;
-      tc_fence_after();
+      bool alive = true;
+      int kb = it.kb0;
+      do {
+        const int acc = local & 1;
+        alive = __all_sync(0xffffffffu, mbar_wait(tfull_bar(acc), (local >> 1) & 1, abort_flag, limit));
+        if (!alive) break;
+        tc_fence_after();
+        const uint32_t tacc = tmem_base + lane_addr + acc * TN;
+        const bool kept = !whole || kb + chain < it.kb1;  // in the slot, not yet the output
 #pragma unroll 1
-      for (int c = half; c < chunks; c += 2) {
-        uint32_t r[32];
-        __syncwarp();  // the load is .aligned, and stores may have left the lanes apart
-        tmem_ld_fragments_sync(tacc + c * 32, r);
-        if (whole) finish(c, r);
-        else slot_dump(my_slot, q, c, static_cast<int>(lane), r);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(tempty_bar(acc), 0));
+        for (int c = half; c < chunks; c += 2) {
+          uint32_t r[32];
+          __syncwarp();  // the load is .aligned, and stores may have left the lanes apart
+          tmem_ld_fragments_sync(tacc + c * 32, r);
+          if (kb > it.kb0) {
+            uint4 t[8];
+            slot_load(my_slot, q, c, static_cast<int>(lane), t);
+            slot_add<I8>(t, r);
+          }
+          if (kept) slot_dump(my_slot, q, c, static_cast<int>(lane), r);
+          else finish(c, r);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(tempty_bar(acc), 0));
+        ++local;
+        kb += chain;
+      } while (kb < it.kb1);
+      if (!alive) break;
       if (!whole) {
         // The last contributor to the tile (per rank) sums the partials in K order.
         const long long t_sk = ring_tile(it) - s.dp_tiles;
@@ -680,7 +698,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!epi.sync(abort_flag, limit)) break;  // reduce_flag has been read
       }
-      ++local;
     }
     if (lane == 0) bulk_wait_group<0>();  // this warp's tile stores have landed
   }

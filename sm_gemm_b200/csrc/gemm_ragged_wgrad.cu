@@ -277,6 +277,7 @@ __global__ void __maxnreg__(128)
   const bool drawn = s.tiles > s.P;
   const int first_drawn = drawn ? static_waves(s.tiles / s.P) * s.P : 0;
   Ring ring{ring_base, rfull_bar, rempty_bar, 0};
+  const int chain = p.c_dtype == 0 ? kChainBlocks : kNoChains;
   auto draws_after = [&](const RingItem& it) { return drawn && it.tile + s.P >= first_drawn; };
 
   if (warp == 0 || warp == 2) {
@@ -351,33 +352,38 @@ __global__ void __maxnreg__(128)
         ok = ring.take(it, abort_flag, limit);
         continue;
       }
-      const int acc = local & 1;
-      const uint32_t acc_phase = (local >> 1) & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait(tempty_bar(acc), acc_phase ^ 1u, abort_flag, limit))) break;
-      tc_fence_after();
-      const uint32_t d_tmem = tmem_base + acc * kTileN;
       bool more = true;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (kb == kb1 - 1) more = ring.take(it, abort_flag, limit);  // behind the MMAs in flight
-        if (!__all_sync(0xffffffffu, mbar_wait(full_bar(stage), phase, abort_flag, limit))) { ok = false; break; }
+      int kb = kb0;
+      do {  // one chain of MMAs on one accumulator
+        const int acc = local & 1;
+        const uint32_t acc_phase = (local >> 1) & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(tempty_bar(acc), acc_phase ^ 1u, abort_flag, limit))) { ok = false; break; }
         tc_fence_after();
-        const uint32_t sa = smem_base + stage * kStageBytes;
-        const int steps = (min(nrow - kb * kBK, kBK) + 15) >> 4;  // of 16 rows, as many as were loaded
-        if (elect_one()) {
+        const uint32_t d_tmem = tmem_base + acc * kTileN;
+        const int first = kb, last = min(kb + chain, kb1);
+        for (; kb < last; ++kb) {
+          if (kb == kb1 - 1) more = ring.take(it, abort_flag, limit);  // behind the MMAs in flight
+          if (!__all_sync(0xffffffffu, mbar_wait(full_bar(stage), phase, abort_flag, limit))) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t sa = smem_base + stage * kStageBytes;
+          const int steps = (min(nrow - kb * kBK, kBK) + 15) >> 4;  // of 16 rows, as many as were loaded
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kBK / 16; ++k)
-            if (k < steps) umma_f16_pair(d_tmem, operand_desc<128, kBK>(sa, 1, k), operand_desc<128, kBK>(sa + kOpBytes, 1, k),
-                          p.idesc, (kb > kb0 || k > 0) ? 1u : 0u);
-          umma_commit_pair(empty_bar(stage), 0x3);
+            for (int k = 0; k < kBK / 16; ++k)
+              if (k < steps)
+                umma_f16_pair(d_tmem, operand_desc<128, kBK>(sa, 1, k), operand_desc<128, kBK>(sa + kOpBytes, 1, k), p.idesc,
+                              (kb > first || k > 0) ? 1u : 0u);
+            umma_commit_pair(empty_bar(stage), 0x3);
+          }
+          __syncwarp();
+          if (++stage == kStages) { stage = 0; phase ^= 1u; }
         }
+        if (!ok) break;
+        if (elect_one()) umma_commit_pair(tfull_bar(acc), 0x3);
         __syncwarp();
-        if (++stage == kStages) { stage = 0; phase ^= 1u; }
-      }
-      if (!ok) break;
-      if (elect_one()) umma_commit_pair(tfull_bar(acc), 0x3);
-      __syncwarp();
-      ++local;
-      ok = more;
+        ++local;
+      } while (kb < kb1);
+      ok = ok && more;
     }
     if (elect_one()) umma_commit_pair(drain_bar, 0x1);
     __syncwarp();
@@ -449,27 +455,35 @@ __global__ void __maxnreg__(128)
         for (int c = 0; c < kEpiCols / 32; ++c) emit(c, v);
         continue;
       }
-      const int acc = local & 1;
-      const uint32_t acc_phase = (local >> 1) & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait(tfull_bar(acc), acc_phase, abort_flag, limit))) break;
-      const uint32_t tacc = tmem_base + lane_addr + acc * kTileN + c_base;
       const int n = s.splits > 1 ? pieces_of(s, (it.nrow + kBK - 1) / kBK) : 1;
       float* my_slot = p.slots + (static_cast<size_t>(cluster) * 2 + rank) * SLOT;
-      tc_fence_after();
+      bool alive = true;
 #pragma unroll 1
-      for (int c = 0; c < kEpiCols / 32; ++c) {
-        uint32_t r[32];
-        __syncwarp();  // the load is .aligned, and stores may have left the lanes apart
-        tmem_ld_32x32b_x32_sync(tacc + c * 32, r);
-        float v[32];
+      for (int kb = it.kb0; kb < it.kb1; kb += chain) {
+        const int acc = local & 1;
+        alive = __all_sync(0xffffffffu, mbar_wait(tfull_bar(acc), (local >> 1) & 1, abort_flag, limit));
+        if (!alive) break;
+        tc_fence_after();
+        const uint32_t tacc = tmem_base + lane_addr + acc * kTileN + c_base;
+        const bool kept = n > 1 || kb + chain < it.kb1;  // in the slot, not yet the output
+#pragma unroll 1
+        for (int c = 0; c < kEpiCols / 32; ++c) {
+          uint32_t r[32];
+          __syncwarp();  // the load is .aligned, and stores may have left the lanes apart
+          tmem_ld_32x32b_x32_sync(tacc + c * 32, r);
+          float v[32];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-        if (n > 1) slot_store<32>(my_slot, r_local, c_base + c * 32, v);
-        else emit(c, v);
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+          if (kb > it.kb0) slot_accumulate<32>(my_slot, r_local, c_base + c * 32, v);
+          if (kept) slot_store<32>(my_slot, r_local, c_base + c * 32, v);
+          else emit(c, v);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(tempty_bar(acc), 0));
+        ++local;
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(tempty_bar(acc), 0));
+      if (!alive) break;
       if (n > 1) {
         if (!epi.sync(abort_flag, limit)) break;
         if (epi_tid == 0) {
@@ -496,7 +510,6 @@ __global__ void __maxnreg__(128)
         }
         if (!epi.sync(abort_flag, limit)) break;  // reduce_flag has been read
       }
-      ++local;
     }
     if (lane == 0) bulk_wait_group<0>();  // this warp's tile stores have landed
   }

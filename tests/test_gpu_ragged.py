@@ -245,6 +245,27 @@ def test_many_experts(cuda_device):
         check_as(BF, dW[e].cpu(), y, s, what=f"dW[{e}]")
 
 
+@pytest.mark.parametrize("split", [False, True])
+def test_long_fp32_sums_round_to_nearest(cuda_device, split):
+    """The tensor core truncates as it accumulates: at most 2^-23 of the sum for every 16
+    products, half of it in the mean, so 64 x 2^-24 for the 1024 products after which the
+    pieces are added rounding to nearest (their own steps, at most 16 here, are below that).
+    One chain would be off by 4.4e-6 for 4096 products and 1.9e-5 for 16384."""
+    tol = 64 * 2.0 ** -24
+    rel = lambda got, ref: float((got.double() - ref).norm() / ref.norm())
+    g = torch.Generator(device="cuda").manual_seed(131)
+    T, K, N = (64, 4096, 512) if split else (2816, 4096, 1536)
+    A = torch.randn(T, K, generator=g, device="cuda").to(BF)
+    W = torch.randn(1, K, N, generator=g, device="cuda").to(BF)
+    off = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    assert rel(sg.gemm_bf16_ragged(A, W, off, out_dtype=F32), A.double() @ W[0].double()) < tol
+    T, K, N = (16384, 264, 520) if split else (16384, 2560, 2048)
+    A = torch.randn(T, K, generator=g, device="cuda").to(BF)
+    D = torch.randn(T, N, generator=g, device="cuda").to(BF)
+    off = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    assert rel(sg.gemm_bf16_ragged_wgrad(A, D, off, out_dtype=F32)[0], A.double().T @ D.double()) < tol
+
+
 def test_output_rows_past_32_bit_offsets(cuda_device):
     """Rows whose first element lies more than 2^31 elements into the output's buffer."""
     T, K, N, ld = 60000, 64, 40, 40000
@@ -482,7 +503,8 @@ def test_small_tiles_in_thousands_of_launches(cuda_device, op):
         D = pitched(normal(121, 1, (T, N), BF).cuda())
         call = lambda out: sg.gemm_bf16_ragged_wgrad(A, D, off, out=out)
         out = pitched(torch.zeros(len(counts), K, N, dtype=HF, device="cuda"))
-    want = call(torch.empty_like(out)).clone()
+    want = call(out).clone()
+    out.zero_()
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
         for _ in range(10):
