@@ -515,6 +515,26 @@ def test_small_tiles_in_thousands_of_launches(cuda_device, op):
     assert torch.equal(out, want)
 
 
+def test_without_programmatic_launches(cuda_device, monkeypatch):
+    """Kernels in stream order give the same bits as kernels that begin early, the bias
+    gradient beside the weight gradient among them."""
+    counts, K, N = GROUPS["40 experts"][0], 136, 264
+    off, T = offsets_of(counts).cuda(), sum(counts)
+    A = pitched(normal(122, 0, (T, K), BF).cuda())
+    W = pitched(normal(122, 1, (len(counts), K, N), BF, K ** -0.5).cuda())
+
+    def run():
+        dbias = torch.full((len(counts), N), 7.0, device="cuda")
+        H = sg.gemm_bf16_ragged(A, W, off, act="silu")
+        dW = sg.gemm_bf16_ragged_wgrad(A, H, off, out_dtype=F32, dbias=dbias)
+        return H.clone(), dW.clone(), dbias
+
+    first = run()
+    monkeypatch.setenv("SMGEMM_PDL", "0")
+    for x, y in zip(first, run()):
+        assert torch.equal(x, y)
+
+
 def test_outputs_of_a_call_on_another_stream(cuda_device):
     """A call given a stream allocates for that stream: its output is not memory that the
     current stream's queued work still uses."""
