@@ -1317,8 +1317,12 @@ smgemm_status gemm_bf16_ragged_wgrad(int E, int64_t T, int64_t N, int64_t K, con
       const CUtensorMapDataType cdt = c_dtype == SMGEMM_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                       : c_dtype == SMGEMM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                                : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-      if (!encode_3d(&m.c, cdt, dB, N, K, E, ldc * sz, (E > 1 ? stride_c : K * ldc) * sz, c_dtype == SMGEMM_F32 ? 16 : 32,
-                     32, CU_TENSOR_MAP_SWIZZLE_64B))
+      p.wide_boxes = c_dtype == SMGEMM_F32 &&
+                     ((reinterpret_cast<uintptr_t>(dB) | static_cast<uintptr_t>(ldc * 4) |
+                       static_cast<uintptr_t>(E > 1 ? stride_c * 4 : 0)) & 31u) != 0;
+      if (!encode_3d(&m.c, cdt, dB, N, K, E, ldc * sz, (E > 1 ? stride_c : K * ldc) * sz,
+                     c_dtype == SMGEMM_F32 && !p.wide_boxes ? 16 : 32, p.wide_boxes ? 16 : 32,
+                     p.wide_boxes ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
         return SMGEMM_ERR_CUDA;
       p.tma_store = 1;
     }

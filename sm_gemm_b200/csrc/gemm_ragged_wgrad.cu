@@ -79,20 +79,27 @@ __device__ __forceinline__ RingItem resolve(const WgradParams& p, const WSched& 
 // Pieces of a tile with kb row blocks.
 __device__ __forceinline__ int pieces_of(const WSched& s, int kb) { return max(1, min(s.splits, kb / kMinKb)); }
 
-// 32 rows (lanes) x 32 columns of a gradient -> dB as TMA tile stores of 64 bytes x 32 rows
-// (two for FP32), staged in alternating 2 KB buffers: the warp goes on while they are
-// written. With 16-byte stores from registers the epilogue bounded small experts' tiles
-// (64 experts of 193 rows, 2048 x 1000 FP32 gradients: 161 us). 16-byte unit j of row r sits
-// at j ^ ((r >> 1) & 3), the map's 64-byte swizzle.
-__device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t buf, int lane, int col, int row0, int e,
-                                          const uint32_t* w) {
+// 32 rows (lanes) x 32 columns of a gradient -> dB as TMA tile stores, staged in alternating
+// 2 KB buffers: the warp goes on while they are written. (With 16-byte stores from registers
+// the epilogue bounded small experts' tiles: 64 experts of 193 rows, 2048 x 1000 FP32
+// gradients, 161 us.) A store is a box of 64 bytes x 32 rows, two of them for FP32, 16-byte
+// unit j of row r at j ^ ((r >> 1) & 3), the map's 64-byte swizzle; or, wide, FP32 in boxes of
+// 128 bytes x 16 rows, unit j at j ^ (r & 7), for rows that do not start on 32-byte sectors:
+// fewer sectors are then written in two parts. 64 experts of one row, 2048 x 2048: 160 us
+// against 192 with wide boxes; 50 experts, 2141 x 2507 (pitch 10032 bytes): 322 against 269.
+template <int W>
+__device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t buf, int lane, bool mine, int r, int col, int row0,
+                                          int e, const uint32_t* w) {
   if (lane == 0) bulk_wait_group_read<kStageBufs - 1>();
   __syncwarp();
+  if (mine) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 64 + 16 * (j ^ ((lane >> 1) & 3))),
-                 "r"(w[4 * j]), "r"(w[4 * j + 1]), "r"(w[4 * j + 2]), "r"(w[4 * j + 3])
-                 : "memory");
+    for (int j = 0; j < W / 4; ++j)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                       buf + r * (4 * W) + 16 * (W == 32 ? j ^ (r & 7) : j ^ ((r >> 1) & 3))),
+                   "r"(w[4 * j]), "r"(w[4 * j + 1]), "r"(w[4 * j + 2]), "r"(w[4 * j + 3])
+                   : "memory");
+  }
   fence_proxy_async_shared();
   __syncwarp();
   if (lane == 0) {
@@ -101,20 +108,26 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t buf, 
   }
 }
 
-__device__ __forceinline__ void store_chunk_tma(const CUtensorMap* map, uint32_t buf, int& turn, int lane, int c_dtype,
+__device__ __forceinline__ void store_chunk_tma(const CUtensorMap* map, const WgradParams& p, uint32_t buf, int& turn, int lane,
                                                 int col0, int row0, int e, const float (&v)[32]) {
   auto next = [&]() { return buf + 2048u * (static_cast<uint32_t>(turn++) % kStageBufs); };
-  if (c_dtype == 0) {
+  if (p.c_dtype == 0) {
     uint32_t w[32];
 #pragma unroll
     for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(v[j]);
-    store_box(map, next(), lane, col0, row0, e, w);
-    store_box(map, next(), lane, col0 + 16, row0, e, w + 16);
+    if (p.wide_boxes) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (row0 + 16 * h < p.K) store_box<32>(map, next(), lane, (lane >> 4) == h, lane & 15, col0, row0 + 16 * h, e, w);
+    } else {
+      store_box<16>(map, next(), lane, true, lane, col0, row0, e, w);
+      store_box<16>(map, next(), lane, true, lane, col0 + 16, row0, e, w + 16);
+    }
   } else {
     uint32_t w[16];
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-      if (c_dtype == 1) {
+      if (p.c_dtype == 1) {
         const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
         w[k] = *reinterpret_cast<const uint32_t*>(&t);
       } else {
@@ -122,7 +135,7 @@ __device__ __forceinline__ void store_chunk_tma(const CUtensorMap* map, uint32_t
         w[k] = *reinterpret_cast<const uint32_t*>(&t);
       }
     }
-    store_box(map, next(), lane, col0, row0, e, w);
+    store_box<16>(map, next(), lane, true, lane, col0, row0, e, w);
   }
 }
 
@@ -451,7 +464,7 @@ __global__ void __maxnreg__(128)
         const int col = col0 + c * 32;
         if (row0 >= p.K || col >= p.N) return;
         if (p.tma_store && (p.whole_units || col + 32 <= p.N))
-          store_chunk_tma(&maps.c, smem_u32(buf), turn, static_cast<int>(lane), p.c_dtype, col, row0, it.e, v);
+          store_chunk_tma(&maps.c, p, smem_u32(buf), turn, static_cast<int>(lane), col, row0, it.e, v);
         else
           store_chunk(e, buf, static_cast<int>(lane), row0, col, v);  // (waits for the buffer's tile stores)
       };

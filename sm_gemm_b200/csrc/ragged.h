@@ -66,8 +66,9 @@ struct WgradParams {
   int c_dtype;
   int tma_store;            // maps.c is there
   int whole_units;          // a row of dB is a whole number of 16-byte units
+  int wide_boxes;           // maps.c stores FP32 in boxes of 32 columns x 16 rows (else 16 x 32)
   long long ldc, stride_c;  // elements between rows / experts of dB
-  float* slots;             // split tiles: [clusters][2 ranks][128][256] partials
+  float* slots;             // pieces of split tiles and FP32 chains: [clusters][2 ranks][128][256]
   unsigned long long* counters;  // [clusters][2]
   unsigned long long gen;
   unsigned long long* ticket;    // draw_ticket's word
