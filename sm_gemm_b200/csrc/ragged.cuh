@@ -77,9 +77,10 @@ struct RaggedPlan {
 __host__ __device__ __forceinline__ int next_cap(int cap) { return cap - (cap > 128 ? 64 : 32); }
 
 // Relative cost per K block of the launch's waves of tiles of `width` rows. A block hardly gets
-// cheaper with the rows: the pair's MMA of 256 features loads its weights at 128 cycles per 16
-// elements of K whatever its N (measured per block, whole GPU: 0.27 us at 32 rows, 0.30 at 128,
-// 0.34 at 256), so lower tiles pay only where they save waves.
+// cheaper with the rows (whole GPU: 0.27 us at 32 rows, 0.30 at 128, 0.34 at 256): the MMA
+// issuer's wait, election and commit take ~475 cycles a block, as long as the MMAs of 230 rows
+// (0.25 us with two clusters on the GPU, 0.23 with one MMA in four, 0.245 without the weights'
+// loads). So lower tiles pay only where they save waves.
 __host__ __device__ __forceinline__ unsigned wave_cycles(int tiles, int width, int P) {
   return static_cast<unsigned>((tiles + P - 1) / P) * static_cast<unsigned>(832 + width);
 }
