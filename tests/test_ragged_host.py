@@ -100,7 +100,7 @@ def test_expert_layouts():
     w = torch.zeros(4, 64, 40)
     assert sg._expert_layout(w, "w") == (sg.ROW_MAJOR, 40, 2560)
     assert sg._expert_layout(w.mT, "w") == (sg.COL_MAJOR, 40, 2560)
-    assert sg._expert_layout(torch.zeros(4, 64, 48)[..., :40], "w") == (sg.ROW_MAJOR, 48, 3072)
+    assert sg._expert_layout(torch.zeros(4, 40, 48)[..., :40], "w") == (sg.ROW_MAJOR, 48, 1920)
     assert sg._expert_layout(w[::2], "w") == (sg.ROW_MAJOR, 40, 5120)
     assert sg._expert_layout(torch.zeros(0, 8, 8), "w")[0] == sg.ROW_MAJOR
     with pytest.raises(ValueError):
