@@ -527,6 +527,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1 && rank == 0) {
     // ---------------------------------------------------------------- MMA issuer
+    // Descriptors of stage 0's first slice of K; the address field counts 16-byte units, so
+    // further stages and slices are additions to it.
+    const int w_mn = I8 ? 0 : p.w_mn_major;
+    const uint64_t w_desc = operand_desc<128, 64>(smem_base, w_mn, 0), x_desc = sdesc_sw128(smem_base + kWBytes, 16, 1024);
+    const uint32_t stage_step = static_cast<uint32_t>(stage_bytes) >> 4, w_step = w_mn ? 2048 >> 4 : 32 >> 4;
     int stage = 0;
     uint32_t phase = 0;
     int local = 0;
@@ -550,15 +555,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (kb == kb1 - 1) more = ring.take(it, abort_flag, limit);  // behind the MMAs in flight
           if (!__all_sync(0xffffffffu, mbar_wait(full_bar(stage), phase, abort_flag, limit))) { ok = false; break; }
           tc_fence_after();
-          const uint32_t sw = smem_base + stage * stage_bytes;
-          const uint32_t sx = sw + kWBytes;
+          const uint64_t wd = w_desc + stage * stage_step, xd = x_desc + stage * stage_step;
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const uint32_t accum = (kb > first || k > 0) ? 1u : 0u;
-              const uint64_t xd = sdesc_sw128(sx + 32 * k, 16, 1024);
-              if constexpr (I8) umma_i8_pair(d_tmem, sdesc_sw128(sw + 32 * k, 16, 1024), xd, idesc, accum);
-              else umma_f16_pair(d_tmem, operand_desc<128, 64>(sw, p.w_mn_major, k), xd, idesc, accum);
+              if constexpr (I8) umma_i8_pair(d_tmem, wd + k * w_step, xd + 2 * k, idesc, accum);
+              else umma_f16_pair(d_tmem, wd + k * w_step, xd + 2 * k, idesc, accum);
             }
             umma_commit_pair(empty_bar(stage), 0x3);
           }
