@@ -78,9 +78,9 @@ __host__ __device__ __forceinline__ int next_cap(int cap) { return cap - (cap > 
 
 // Relative cost per K block of the launch's waves of tiles of `width` rows. A block hardly gets
 // cheaper with the rows (whole GPU: 0.27 us at 32 rows, 0.30 at 128, 0.34 at 256): the MMA
-// issuer's wait, election and commit take ~475 cycles a block, as long as the MMAs of 230 rows
-// (0.25 us with two clusters on the GPU, 0.23 with one MMA in four, 0.245 without the weights'
-// loads). So lower tiles pay only where they save waves.
+// issuer's wait, election and commit take ~435 cycles a block, as long as the MMAs of 220 rows
+// (0.23 us with two clusters on the GPU; hardly less with one MMA in four, or without the
+// weights' loads). So lower tiles pay only where they save waves.
 __host__ __device__ __forceinline__ unsigned wave_cycles(int tiles, int width, int P) {
   return static_cast<unsigned>((tiles + P - 1) / P) * static_cast<unsigned>(832 + width);
 }
